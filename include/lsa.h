@@ -578,6 +578,59 @@ int lsa_gather_tokens(const void* k_buf, const void* v_buf, int64_t buf_chunks, 
                       const int32_t* sel, const int32_t* cu_sel, int B, int max_sel, void* k_out,
                       void* v_out, int64_t out_chunks, int32_t* cu_units, void* stream);
 
+/*
+ * lsa_qk_norm_rope -- the norms of queries and keys for each head and the
+ * rotary positions, in one pass over the rows of the fused projection; the
+ * step before every attention call (its q_out is their q, its k_out and v_out
+ * are lsa_sparse_decode_attn_append's k_new and v_new).  For token t, row t of
+ * qkv holds 64 query heads, 8 key heads and 8 value heads of 128 dims each.
+ * For every query head (w = q_weight) and key head (w = k_weight):
+ *
+ *   y = x * w / sqrt(mean(x^2) + eps)          (y = x when the weight is NULL)
+ *   for i < rot_dim / 2, with angle = positions[t] * inv_freq[i]:
+ *     a' = rope_scale * (a cos(angle) - b sin(angle))
+ *     b' = rope_scale * (b cos(angle) + a sin(angle))
+ *
+ * where (a, b) are dims (i, i + rot_dim / 2) of y, or dims (2i, 2i + 1) with
+ * LSA_ROPE_INTERLEAVED; dims rot_dim .. 127 keep y.  The value heads are
+ * copied.  fp32, rounded once to bf16; the angle is formed in fp64, so far
+ * positions keep their phase.  Scaled rotations for long contexts are a matter
+ * of inv_freq and rope_scale (the Python binding's rope_frequencies).
+ *   qkv        device bf16 [T] rows of 80 * 128 values, row_stride (>= 10240, a
+ *              multiple of 8) values apart
+ *   q_weight, k_weight  device fp32 [128] or NULL, 16-byte aligned
+ *   positions  device int32 [T]; inv_freq device fp32 [rot_dim / 2]
+ *   rot_dim    0 (no rotation; positions and inv_freq may be NULL) to 128, a
+ *              multiple of 8
+ *   q_out      device bf16 [T][64][128]; k_out, v_out device bf16 [T][8][128]
+ *              (v_out may be NULL: the value heads are not copied)
+ * The outputs must not overlap qkv.  T > 0.  No device errors.
+ */
+#define LSA_ROPE_INTERLEAVED 1u
+int lsa_qk_norm_rope(const void* qkv, int64_t row_stride, int64_t T, const float* q_weight,
+                     const float* k_weight, float eps, const int32_t* positions,
+                     const float* inv_freq, int rot_dim, float rope_scale, unsigned int flags,
+                     void* q_out, void* k_out, void* v_out, void* stream);
+
+/*
+ * lsa_qk_norm_rope_pool -- lsa_qk_norm_rope with the key and value rows written
+ * into the pools: token t becomes position p = cache_pos[t] of sequence
+ * b = seq_ids[t], row p % 64 of chunk slot(b, p / 64) of every KV head.  A token
+ * with cache_pos[t] < 0 (padding) is not written; its query is.  Two tokens of
+ * one call must not name the same row.
+ *   k_pool, v_pool  device bf16 [n_slots][8][64][128]
+ *   chunk_table     device int32 [B][max_chunks], or NULL (identity layout)
+ *   seq_ids, cache_pos  device int32 [T]; cache_pos may be positions itself
+ * Device errors: BAD_COUNT (seq_ids[t] outside [0, B)), BAD_CHUNK (cache_pos[t]
+ * beyond max_chunks chunks), BAD_SLOT: that token's K and V are not written.
+ */
+int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const float* q_weight,
+                          const float* k_weight, float eps, const int32_t* positions,
+                          const float* inv_freq, int rot_dim, float rope_scale,
+                          unsigned int flags, void* q_out, void* k_pool, void* v_pool,
+                          int64_t n_slots, const int32_t* chunk_table, const int32_t* seq_ids,
+                          const int32_t* cache_pos, int B, int max_chunks, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -77,6 +77,8 @@ def _load():
         "lsa_attn_workspace_size": ([I], S),
         "lsa_sparse_decode_attn": ([P, P, P, I64, P, I, F, P, P, S, ctypes.c_uint, P], I),
         "lsa_sparse_decode_attn_noalloc": ([P, P, P, I64, P, I, F, P, P], I),
+        "lsa_qk_norm_rope": ([P, I64, I64, P, P, F, P, P, I, F, ctypes.c_uint, P, P, P, P], I),
+        "lsa_qk_norm_rope_pool": ([P, I64, I64, P, P, F, P, P, I, F, ctypes.c_uint, P, P, P, I64, P, P, P, I, I, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -541,7 +543,109 @@ def lsa_sparse_decode_attn_noalloc(q, k_buf, v_buf, cu_kept, out, softmax_scale=
         _ptr(q), _ptr(k_buf), _ptr(v_buf), _buf_chunks(k_buf, "k_buf"), _ptr(cu_kept), B, scale, _ptr(out), _stream(stream)))
 
 
+ROPE_INTERLEAVED = 1
+
+
+def _here(*tensors):
+    """The tensors that are given live on the current device, whose stream the call uses."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _pool(t: torch.Tensor, name: str) -> int:
+    """Slots of a KV pool [slots, 8, 64, 128]."""
+    _need(t, name, torch.bfloat16)
+    if t.dim() != 4 or tuple(t.shape[1:]) != (NUM_KV_HEADS, CHUNK_TOKENS, HEAD_DIM):
+        raise ValueError(f"{name} must be a pool [slots, 8, 64, 128], got {tuple(t.shape)}")
+    return int(t.shape[0])
+
+
+def _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight):
+    """Checks of the arguments both forms share; the number of tokens."""
+    if not isinstance(qkv, torch.Tensor) or qkv.dtype != torch.bfloat16 or not qkv.is_cuda:
+        raise TypeError("qkv must be a CUDA bfloat16 tensor")
+    width = (NUM_Q_HEADS + 2 * NUM_KV_HEADS) * HEAD_DIM
+    if qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
+        raise ValueError(f"qkv must be [T, {width}] with contiguous rows")
+    T = qkv.shape[0]
+    _need(q_out, "q_out", torch.bfloat16)
+    if tuple(q_out.shape) != (T, NUM_Q_HEADS, HEAD_DIM):
+        raise ValueError("q_out must be [T, 64, 128]")
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32)
+        _need(positions, "positions", torch.int32)
+        if inv_freq.dim() != 1 or positions.numel() != T:
+            raise ValueError("inv_freq must be [rot_dim / 2] and positions [T]")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, n, torch.float32)
+            if w.numel() != HEAD_DIM:
+                raise ValueError(f"{n} must have 128 values")
+    _here(qkv, positions, inv_freq, q_out, q_weight, k_weight)
+    return T
+
+
+def _row_stride(qkv) -> int:
+    """Elements between rows; torch leaves the stride of a single row open."""
+    return qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
+
+
+def lsa_qk_norm_rope(qkv, positions, inv_freq, q_out, k_out, v_out=None, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, rope_scale=1.0, stream=None):
+    """Head norms and rotary positions of a fused projection's rows qkv [T, 80 * 128] (rows may lie further
+    apart): q_out [T, 64, 128], k_out and v_out [T, 8, 128], bf16.
+
+    Rotates the first 2 * inv_freq.numel() dims of each query and key head by positions * inv_freq
+    (rope_frequencies makes the table; None: no rotation), after the RMS norm with q_weight / k_weight fp32 [128]
+    (None: no norm).  v_out None: the value heads are not copied."""
+    T = _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None or n == "k_out":
+            _need(t, n, torch.bfloat16)
+            if tuple(t.shape) != (T, NUM_KV_HEADS, HEAD_DIM):
+                raise ValueError(f"{n} must be [T, 8, 128]")
+    _here(k_out, v_out)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _check("lsa_qk_norm_rope", _load().lsa_qk_norm_rope(
+        _ptr(qkv), _row_stride(qkv), T, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot,
+        float(rope_scale), ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), _ptr(k_out), _ptr(v_out),
+        _stream(stream)))
+
+
+def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks,
+                          q_weight=None, k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
+    """lsa_qk_norm_rope with token t's K and V written to position cache_pos[t] of sequence seq_ids[t] in the
+    pools [slots, 8, 64, 128] (chunk_table [B, max_chunks], or None for the identity layout; cache_pos < 0: not
+    written)."""
+    T = _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight)
+    n_slots = _pool(k_pool, "k_pool")
+    if _pool(v_pool, "v_pool") != n_slots:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    for t, n in ((seq_ids, "seq_ids"), (cache_pos, "cache_pos")):
+        _need(t, n, torch.int32)
+        if t.numel() != T:
+            raise ValueError(f"{n} must be [T]")
+    if chunk_table is not None:
+        _need(chunk_table, "chunk_table", torch.int32)
+        if chunk_table.dim() != 2 or chunk_table.shape[1] != max_chunks:
+            raise ValueError("chunk_table must be [B, max_chunks]")
+    elif max_chunks <= 0:
+        raise ValueError("max_chunks must be positive")
+    B = chunk_table.shape[0] if chunk_table is not None else max(1, n_slots // int(max_chunks))
+    _here(k_pool, v_pool, chunk_table, seq_ids, cache_pos)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _check("lsa_qk_norm_rope_pool", _load().lsa_qk_norm_rope_pool(
+        _ptr(qkv), _row_stride(qkv), T, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot,
+        float(rope_scale), ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), _ptr(k_pool), _ptr(v_pool), n_slots,
+        _ptr(chunk_table), _ptr(seq_ids), _ptr(cache_pos), B, int(max_chunks), _stream(stream)))
+
+
+from .rope import rope_frequencies  # noqa: E402
+
 __all__ = [
+    "lsa_qk_norm_rope", "lsa_qk_norm_rope_pool", "rope_frequencies",
     "LsaError", "lib", "read_device_status", "decode_status", "lsa_index_score", "lsa_topk_chunks",
     "lsa_threshold_chunks",
     "lsa_gather_chunks", "lsa_fetch_from_host", "lsa_fetch_from_host_delta", "lsa_fetch_from_host_copy",
