@@ -631,6 +631,92 @@ int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const 
                           int64_t n_slots, const int32_t* chunk_table, const int32_t* seq_ids,
                           const int32_t* cache_pos, int B, int max_chunks, void* stream);
 
+/*
+ * lsa_window_attn -- attention with a sliding window and a few first tokens
+ * that stay visible, read in place from the pools: the layers whose cache is
+ * the recent context, beside those whose cache is recalled.  Sequence b has
+ * seq_len[b] cached tokens, its queries (rows cu_q[b] .. cu_q[b+1]-1 of q) are
+ * its last ones, nq = cu_q[b+1] - cu_q[b]: one for a decode step, many for a
+ * prompt or a piece of one, mixed freely in a batch.  The query at position p
+ * sees the keys j <= p with j > p - window or j < n_sink, every 8 consecutive
+ * query heads on their KV head:
+ *
+ *   out[t,h,:] = sum_j softmax_j(scale * q[t,h,:] . k_j) v_j
+ *
+ * A query that sees nothing (nq > seq_len: positions below 0) gets zeros.  A
+ * window of at least seq_len is causal attention over all cached tokens.
+ *   q           device bf16 [T][64][128]; out device bf16 [T][64][128] (fp32
+ *               sums and softmax; the probabilities are rounded once to bf16
+ *               for the tensor cores, the output once).  Rows at or past
+ *               cu_q[B] are left as they were.
+ *   k_pool, v_pool  device bf16 [n_slots][8][64][128], n_slots < 2^22
+ *   chunk_table device int32 [B][max_chunks] or NULL (identity layout); chunks
+ *               that no query sees are not looked up: a table may hold -1 where
+ *               a chunk was given back
+ *   cu_q        device int32 [B+1]; seq_len device int32 [B]
+ *   max_q       at least every nq (the size of the partials)
+ *   window >= 1, n_sink >= 0; softmax_scale > 0
+ *   workspace   device, >= lsa_window_attn_workspace_size(B, max_q) bytes,
+ *               16-byte aligned, no initialisation; calls that may overlap on
+ *               the GPU need workspaces of their own
+ * K and V rows that no query of a sequence sees may hold anything, NaN
+ * included; a value of V that is not finite and that one query sees may reach
+ * the other queries of the same 32 (a prompt's) that do not.
+ * The work is cut into equal shares whatever the batch, and the partials of a
+ * query are joined in a fixed order: repeated calls are bit-identical.  Two
+ * kernels, both programmatic dependents of their predecessor.  Device errors:
+ * CAPACITY (cu_q not starting at 0, decreasing, past T, or an nq above max_q:
+ * nothing is computed), BAD_COUNT (seq_len outside [0, 64 max_chunks]: that
+ * sequence's rows are zeros), BAD_SLOT (that chunk is read as zeros), TIMEOUT.
+ */
+#define LSA_POOL_ATTN_MAX_CTAS 160
+size_t lsa_window_attn_workspace_size(int B, int max_q);
+int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_pool,
+                    int64_t n_slots, const int32_t* chunk_table, const int32_t* cu_q,
+                    const int32_t* seq_len, int B, int max_chunks, int max_q, int window,
+                    int n_sink, float softmax_scale, void* out, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * lsa_prefix_decode_attn -- one decode step of a batch whose groups share a
+ * long prefix (a system prompt, a document, the samples of one prompt).  Group
+ * n holds the sequences cu_group[n] .. cu_group[n+1]-1; they attend the
+ * prefix_len[n] tokens of the group's prefix and then suffix_len[b] tokens of
+ * their own, whose chunks the tables name:
+ *
+ *   out[b,h,:] = sum_j softmax_j(scale * q[b,h,:] . k_j) v_j,  j over both
+ *
+ * The prefix is read once per KV head for every 32 sequences of its group and
+ * multiplied with all of their queries together.  Sequences from
+ * cu_group[n_groups] on belong to no group: they attend their own tokens only.
+ * A sequence with no token at all gets zeros.
+ *   q            device bf16 [B][64][128]; out device bf16 [B][64][128]
+ *                (rounded as by lsa_window_attn)
+ *   prefix_table device int32 [n_groups][max_prefix_chunks], slots of the
+ *                prefix's chunks; cu_group device int32 [n_groups+1];
+ *                prefix_len device int32 [n_groups].  n_groups 0: all may be NULL
+ *   chunk_table  device int32 [B][max_chunks] or NULL (identity layout), slots
+ *                of the sequence's own chunks (its own token 0 is token 0 of
+ *                chunk 0, whatever the prefix's length); suffix_len device
+ *                int32 [B]
+ *   workspace    device, >= lsa_prefix_attn_workspace_size(B, n_groups) bytes,
+ *                16-byte aligned, no initialisation; calls that may overlap on
+ *                the GPU need workspaces of their own
+ * Rows of a chunk past a length may hold anything.  Deterministic.  Two
+ * kernels, both programmatic dependents of their predecessor.  Device errors:
+ * CAPACITY (cu_group not starting at 0, decreasing or past B: nothing is
+ * computed), BAD_COUNT (a length out of range: that prefix, or that
+ * sequence's own tokens, count as none), BAD_SLOT (that chunk is read as
+ * zeros), TIMEOUT.
+ */
+size_t lsa_prefix_attn_workspace_size(int B, int n_groups);
+int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool, int64_t n_slots,
+                           const int32_t* prefix_table, const int32_t* cu_group,
+                           const int32_t* prefix_len, int n_groups, int max_prefix_chunks,
+                           const int32_t* chunk_table, const int32_t* suffix_len, int B,
+                           int max_chunks, float softmax_scale, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

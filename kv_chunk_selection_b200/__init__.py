@@ -77,6 +77,10 @@ def _load():
         "lsa_attn_workspace_size": ([I], S),
         "lsa_sparse_decode_attn": ([P, P, P, I64, P, I, F, P, P, S, ctypes.c_uint, P], I),
         "lsa_sparse_decode_attn_noalloc": ([P, P, P, I64, P, I, F, P, P], I),
+        "lsa_window_attn_workspace_size": ([I, I], S),
+        "lsa_window_attn": ([P, I64, P, P, I64, P, P, P, I, I, I, I, I, F, P, P, S, P], I),
+        "lsa_prefix_attn_workspace_size": ([I, I], S),
+        "lsa_prefix_decode_attn": ([P, P, P, I64, P, P, P, I, I, P, P, I, I, F, P, P, S, P], I),
         "lsa_qk_norm_rope": ([P, I64, I64, P, P, F, P, P, I, F, ctypes.c_uint, P, P, P, P], I),
         "lsa_qk_norm_rope_pool": ([P, I64, I64, P, P, F, P, P, I, F, ctypes.c_uint, P, P, P, I64, P, P, P, I, I, P], I),
     }
@@ -642,10 +646,100 @@ def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk
         _ptr(chunk_table), _ptr(seq_ids), _ptr(cache_pos), B, int(max_chunks), _stream(stream)))
 
 
+def new_window_attn_workspace(B: int, max_q: int, device=None) -> torch.Tensor:
+    """A workspace for lsa_window_attn with up to ``max_q`` queries per sequence (it needs no initialisation)."""
+    n = int(_load().lsa_window_attn_workspace_size(int(B), int(max_q)))
+    if n == 0:
+        raise ValueError("unsupported batch")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _pool_attn_args(q, k_pool, v_pool, chunk_table, lengths, max_chunks, out, workspace, name):
+    """Checks of the arguments both pool attentions share; slots, sequences and chunks per table row."""
+    _need(q, "q", torch.bfloat16)
+    _need(out, "out", torch.bfloat16)
+    _need(workspace, "workspace", torch.uint8)
+    _need(lengths, name, torch.int32)
+    if q.dim() != 3 or tuple(q.shape[1:]) != (NUM_Q_HEADS, HEAD_DIM) or out.shape != q.shape:
+        raise ValueError("q and out must be [rows, 64, 128]")
+    n_slots = _pool(k_pool, "k_pool")
+    if _pool(v_pool, "v_pool") != n_slots:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    B = lengths.numel()
+    if chunk_table is not None:
+        _need(chunk_table, "chunk_table", torch.int32)
+        if chunk_table.dim() != 2 or chunk_table.shape[0] != B or (max_chunks is not None
+                                                                   and chunk_table.shape[1] != max_chunks):
+            raise ValueError("chunk_table must be [B, max_chunks]")
+        max_chunks = chunk_table.shape[1]
+    elif max_chunks is None:
+        raise ValueError("the identity layout (no chunk_table) needs max_chunks")
+    _here(q, k_pool, v_pool, chunk_table, lengths, out, workspace)
+    return n_slots, B, int(max_chunks)
+
+
+def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, max_q, window, n_sink, out, workspace,
+                    softmax_scale=None, stream=None):
+    """out[t] = attention of query row t over the last ``window`` tokens up to its own and the first ``n_sink``.
+
+    Sequence b's queries are rows cu_q[b] .. cu_q[b+1]-1 of q [T, 64, 128] and the last of its seq_len[b] cached
+    tokens, which the pools [slots, 8, 64, 128] hold by chunk_table [B, max_chunks] (None: identity layout); at
+    most ``max_q`` per sequence.  out is bf16 like q; workspace from new_window_attn_workspace(B, max_q)."""
+    n_slots, B, max_chunks = _pool_attn_args(q, k_pool, v_pool, chunk_table, seq_len, int(max_chunks), out, workspace,
+                                             "seq_len")
+    _need(cu_q, "cu_q", torch.int32)
+    if cu_q.numel() != B + 1:
+        raise ValueError("cu_q must be [B + 1]")
+    _here(cu_q)
+    scale = 1.0 / math.sqrt(HEAD_DIM) if softmax_scale is None else float(softmax_scale)
+    _check("lsa_window_attn", _load().lsa_window_attn(
+        _ptr(q), q.shape[0], _ptr(k_pool), _ptr(v_pool), n_slots, _ptr(chunk_table), _ptr(cu_q), _ptr(seq_len), B,
+        max_chunks, int(max_q), int(window), int(n_sink), scale, _ptr(out), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+
+
+def new_prefix_attn_workspace(B: int, n_groups: int, device=None) -> torch.Tensor:
+    """A workspace for lsa_prefix_decode_attn (it needs no initialisation)."""
+    n = int(_load().lsa_prefix_attn_workspace_size(int(B), int(n_groups)))
+    if n == 0:
+        raise ValueError("unsupported batch")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len, chunk_table, suffix_len, out, workspace,
+                           softmax_scale=None, max_chunks=None, stream=None):
+    """One decode step of a batch whose groups share prefixes: sequence b of group n (cu_group[n] <= b <
+    cu_group[n+1]) attends the prefix_len[n] tokens of the chunks prefix_table[n] and then the suffix_len[b] tokens
+    of its own chunks chunk_table[b], all in the pools [slots, 8, 64, 128].
+
+    q and out [B, 64, 128] bf16; prefix_table, cu_group and prefix_len None: no sequence has a prefix; chunk_table
+    None: the identity layout with ``max_chunks`` chunks per sequence.  Workspace from new_prefix_attn_workspace."""
+    n_slots, B, max_chunks = _pool_attn_args(q, k_pool, v_pool, chunk_table, suffix_len, max_chunks, out, workspace,
+                                             "suffix_len")
+    if q.shape[0] != B:
+        raise ValueError("q must be [B, 64, 128]")
+    groups = chunks = 0
+    if prefix_table is not None:
+        for t, n in ((prefix_table, "prefix_table"), (cu_group, "cu_group"), (prefix_len, "prefix_len")):
+            _need(t, n, torch.int32)
+        if prefix_table.dim() != 2:
+            raise ValueError("prefix_table must be [n_groups, max_prefix_chunks]")
+        groups, chunks = prefix_table.shape
+        if cu_group.numel() != groups + 1 or prefix_len.numel() != groups:
+            raise ValueError("cu_group must be [n_groups + 1] and prefix_len [n_groups]")
+        _here(prefix_table, cu_group, prefix_len)
+    scale = 1.0 / math.sqrt(HEAD_DIM) if softmax_scale is None else float(softmax_scale)
+    _check("lsa_prefix_decode_attn", _load().lsa_prefix_decode_attn(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), n_slots, _ptr(prefix_table), _ptr(cu_group), _ptr(prefix_len), groups, chunks,
+        _ptr(chunk_table), _ptr(suffix_len), B, max_chunks, scale, _ptr(out), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+
+
 from .rope import rope_frequencies  # noqa: E402
 
 __all__ = [
-    "lsa_qk_norm_rope", "lsa_qk_norm_rope_pool", "rope_frequencies",
+    "lsa_qk_norm_rope", "lsa_qk_norm_rope_pool", "rope_frequencies", "lsa_window_attn", "new_window_attn_workspace",
+    "lsa_prefix_decode_attn", "new_prefix_attn_workspace",
     "LsaError", "lib", "read_device_status", "decode_status", "lsa_index_score", "lsa_topk_chunks",
     "lsa_threshold_chunks",
     "lsa_gather_chunks", "lsa_fetch_from_host", "lsa_fetch_from_host_delta", "lsa_fetch_from_host_copy",
