@@ -18,16 +18,17 @@
 // chip; a tile that a cut splits leaves one partial per CTA (normalised rows
 // and their log-sum-exps), which a second kernel folds in CTA order.
 //
-// Roles of a CTA (11 warps):
+// Roles of a CTA (12 warps):
 //   warps 0-3, 4-7  two softmax warpgroups, a thread per row: the scores of a
 //                   unit come from TMEM, the probabilities go back to TMEM in
 //                   the scores' place as bf16.  The running maximum is only
 //                   raised when it grows by more than 2^8 (the sums stay
 //                   exact, the accumulator is rescaled rarely);
-//   warp 8          issues the tcgen05.mma: S = Q K^T (128 x 64 x 128), and
-//                   O += P V (128 x 128 x 64) with P read from TMEM;
-//   warp 9          streams the units with TMA into a ring of 5 stages;
-//   warp 10         loads the query tile of the next segment.
+//   warps 8, 9      issue the tcgen05.mma of a warpgroup each: S = Q K^T (128 x
+//                   64 x 128), and O += P V (128 x 128 x 64) with P from TMEM;
+//   warp 10         streams the units with TMA into a ring of 4 stages;
+//   warp 11         walks the list, a few segments ahead of the others, and
+//                   loads the query tiles.
 // A tile of more than 16 queries is "wide": each warpgroup has 16 queries (128
 // rows) and both use every unit.  A smaller tile is "narrow": both warpgroups
 // have the same rows and take alternate units, so that the softmax of one unit
@@ -52,15 +53,16 @@ namespace pool {
 constexpr int kWideQ = 32;                   // queries of a tile
 constexpr int kHalfQ = 16;                   // queries of a warpgroup: 16 x 8 heads = 128 rows
 constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kQueryWarp = 10;
-constexpr int kThreads = 11 * 32;
-constexpr int kStages = 5;
+constexpr int kMmaWarp = 8;                  // and 9: one for each softmax warpgroup
+constexpr int kLoadWarp = 10, kPlanWarp = 11;
+constexpr int kThreads = 12 * 32;
+constexpr int kStages = 4;
 constexpr int kBoxBytes = 8192;              // 64 tokens x 64 dims
 constexpr int kStageBytes = 4 * kBoxBytes;   // K dims 0-63, 64-127, V dims 0-63, 64-127
 constexpr int kQBoxBytes = 16384;            // 128 rows x 64 dims
 constexpr int kQTileBytes = 2 * kQBoxBytes;
-constexpr int kSmemBytes = kStages * kStageBytes + 2 * kQTileBytes + 2 * 2 * 128 * 4 + 256;
-static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+constexpr int kTurnBytes = 4096;             // a warp's rows on their way out: 32 rows x 128 bytes
+constexpr int kAhead = 8;                    // places for segments that the planner is ahead
 constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
 constexpr float kRaise = 8.f;                // growth of the maximum (log2) that rescales the accumulator
 constexpr int kSCols = 64, kOCol0 = 256;     // TMEM: S[w][b] at (2 w + b) * 64, O[w] at 256 + 128 w
@@ -81,15 +83,24 @@ struct Plan {
   __device__ int lists() const { return prefix_mode ? groups + B : B; }
 };
 
-// Partials: `rows_cap` rows per record.
+// Partials.  A CTA's first and last segment can be part of a tile: they have a
+// record each, slots 2c and 2c + 1, of rows_cap rows (query x head).  In window
+// mode a whole tile goes straight to the output; in prefix mode its rows have
+// places of their own, 64 per sequence for its prefix and 64 for its own tokens,
+// after which the slots follow.
 struct Work {
-  float* o;          // [record rows][128]
-  float* lse;        // [record rows]
-  int64_t* base;     // prefix mode: first unit of each list, then the total; window mode: the total
-  int4* seg;         // window mode: [2 * kMaxCtas][2] first and last segment of each CTA
-  int* ok;           // [1]: the offsets were valid
+  float* o;          // [rows][128], normalised
+  float* lse;        // [rows], base 2
+  int4* seg;         // window mode: [2 * kMaxCtas], a slot's tile: first query, KV head and queries,
+                     // first and last CTA, slot of the first CTA's record + 1 (0: nothing to fold)
+  int* ends;         // prefix mode: [4][8 B], by (sequence, KV head): first and last partial of the
+                     // prefix, of the own tokens
+  int* ok;           // prefix mode: the offsets were valid
   int rows_cap;
 };
+// The first partial of a (sequence, KV head): CTA, slot 2c + bit, the query's
+// place in the tile, or that the rows are in their own place; kNone: no partial.
+constexpr int kEndSlot = 1 << 8, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
 
 // The queries and the keys of one list: a sequence, or a group over its prefix.
 struct List {
@@ -155,13 +166,17 @@ __device__ __forceinline__ int64_t units_before(const Plan& p, const List& s, in
   return n;
 }
 
+// A 64-bit quotient, in 32 bits where the operands allow it (five times faster).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 struct Partition {
   int64_t base, rem;
-  __device__ Partition(int64_t total, int G) : base(total / G), rem(total % G) {}
+  __device__ Partition(int64_t total, int G) : base(quotient(total, G)), rem(total - base * G) {}
   __device__ int64_t start(int c) const { return c * base + (c < rem ? c : rem); }
   __device__ int cta_of(int64_t u) const {
     const int64_t big = rem * (base + 1);
-    return static_cast<int>(u < big ? u / (base + 1) : rem + (u - big) / base);
+    return static_cast<int>(u < big ? quotient(u, base + 1) : rem + quotient(u - big, base));
   }
 };
 
@@ -195,12 +210,12 @@ struct Cursor {
     s = load_list(p, v);
     tiles = tiles_of(s);
   }
-  // At unit r of list v.
-  __device__ void start(const Plan& p, int list, int64_t r) {
+  // At unit r of list `list`, whose KV heads have per_head units each.
+  __device__ void start(const Plan& p, int list, const List& l, int64_t per_head, int64_t r) {
     v = list;
-    set_list(p);
-    const int64_t per_head = units_before(p, s, tiles);
-    g = static_cast<int>(r / per_head);
+    s = l;
+    tiles = tiles_of(s);
+    g = static_cast<int>(quotient(r, per_head));
     r -= g * per_head;
     int lo = 0, hi = tiles - 1;
     while (lo < hi) {
@@ -235,11 +250,60 @@ __device__ __forceinline__ uint64_t lowest(int x) {
   return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1;
 }
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+// Barriers and copies by shared address: a generic pointer takes two registers
+// and a conversion at every use.
+__device__ __forceinline__ void bar_init(uint32_t bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity) {
+  unsigned ok;
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits, at most kWaitLimitNs, or until another role has given up; the same
+// answer in every lane, so that the warp's collective instructions stay whole.
+// `abort_flag`: 0, or 1 once a wait of the CTA ran out.
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, unsigned parity, uint32_t abort_flag, unsigned* status) {
+  const unsigned long long t0 = globaltimer_ns();
+  for (unsigned it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    if ((it & 63u) == 0) {
+      int given_up;
+      asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(given_up) : "r"(abort_flag) : "memory");
+      const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+      if (__any_sync(0xffffffffu, given_up || late)) {
+        if (!given_up) set_status(status, LSA_DEV_ERR_TIMEOUT);
+        asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity, uint32_t abort_flag, unsigned* status) {
+  if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+  return bar_wait_slow(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
@@ -247,23 +311,52 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             bool accumulate) {
+// One lane of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Shared-memory descriptors as a constant upper word and a lower word that holds
+// the address in 16-byte steps (and the leading offset), so that a tile's k-steps
+// are additions.  Both operands use the 128-byte swizzle, with 8-row groups 1024
+// bytes apart (stride offset).  K-major (Q, K): the leading offset is unused.
+// V is the N x K operand (N = dims, K = tokens) stored token by token, N
+// contiguous: its 64-dim boxes are 8192 bytes apart (leading offset).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_kmajor(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_v(uint32_t saddr) {
+  return ((saddr >> 4) & 0x3FFFu) | (static_cast<uint32_t>(kBoxBytes >> 4) << 16);
+}
+// The warp runs these together and the lane with `leader` set issues: a branch
+// around them would keep the operands out of the uniform registers that they
+// are read from.
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
-// Shared-memory descriptor of V as the N x K operand (N = dims, K = tokens),
-// stored token by token (N contiguous) with the 128-byte swizzle: 64-dim boxes
-// 8192 bytes apart (leading offset), 8-token groups 1024 bytes apart (stride).
-__device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr) {
-  return (static_cast<uint64_t>((saddr >> 4) & 0x3FFFu)) | (static_cast<uint64_t>(kBoxBytes >> 4) << 16) |
-         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
-         (static_cast<uint64_t>(2u) << 61);
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
 }
 constexpr uint32_t kIdescS = umma_idesc_bf16_f32(128, kChunkTokens);
 constexpr uint32_t kIdescO = umma_idesc_bf16_f32(128, kHeadDim) | (1u << 16);   // B with N contiguous
@@ -301,6 +394,44 @@ __device__ __forceinline__ void tmem_wait_ld(float* v, int n) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 operations in one instruction, and the maximum of three.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float v;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  return v;
+}
+
+// Registers per thread from here on, for a warpgroup whose warps all say so: the
+// block's 384 x 168 go 208 + 208 to the softmax warpgroups and 88 to the others.
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the shares come out of the block's own registers");
+
 // Exclusive prefix sum of `x` over the block (kWarps warps) and the total.
 template <int kWarps>
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sm, int64_t* total) {
@@ -323,386 +454,482 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sm, int64_t* t
   return before + inc - x;
 }
 
+// A segment: the units of one tile that this CTA has.  The planner warp writes
+// them to shared memory a few ahead, so that no other role walks the list or
+// waits for its loads.
+struct Seg {
+  int units;                 // 0: the list has ended
+  int flags;                 // kSegWide ...
+  int j0;                    // its first unit in the tile
+  int cnt, row, head;        // the tile's queries, the first one's row of q, the first query head
+  int first, low;            // chunk of unit j: j < first ? j : low + j - first
+  int f0, f1, f2;            // units that every query sees whole: j < f0 and f1 <= j <= f2
+  int p0, len;               // window mode: position of the first query; prefix mode: tokens
+  int g;
+  const int32_t* table;
+  int64_t ident;
+};
+constexpr int kSegWide = 1, kSegEmpty = 2, kSegAgain = 4, kSegGroup = 8, kSegWhole = 16;
+
+// Shared memory, from a 1024-byte boundary.
+constexpr int kQAt = kStages * kStageBytes, kTurnAt = kQAt + 2 * kQTileBytes, kMlAt = kTurnAt + 8 * kTurnBytes;
+constexpr int kSegAt = kMlAt + 2 * 2 * 128 * 4, kBarAt = kSegAt + kAhead * static_cast<int>(sizeof(Seg));
+// Barriers, 8 bytes each.
+constexpr int kFull = kBarAt, kEmpty = kFull + 8 * kStages;            // ring stages
+constexpr int kSFull = kEmpty + 8 * kStages;                            // [2 warpgroups][2 buffers] scores are there
+constexpr int kPFull = kSFull + 32, kODone = kPFull + 32;               // probabilities are; the product that read them is done
+constexpr int kQFull = kODone + 32, kQEmpty = kQFull + 8;
+constexpr int kSegFull = kQEmpty + 8, kSegEmptied = kSegFull + 8 * kAhead;
+constexpr int kMeet = kSegEmptied + 8 * kAhead, kReady = kMeet + 8;     // both warpgroups; the scratch has been read
+constexpr int kDrain = kReady + 8;                                      // [2]
+constexpr int kTmemAt = kDrain + 16, kAbortAt = kTmemAt + 4;
+constexpr int kSmemBytes = kAbortAt + 4;
+static_assert(kSmemBytes <= 232448 && sizeof(Seg) % 8 == 0, "shared memory of one CTA");
+
 __global__ void __launch_bounds__(kThreads, 1)
 pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1, const Plan plan,
                  const Work work, float scale_log2, __nv_bfloat16* __restrict__ out, unsigned* status) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sm = smem_u32(smem);
+  const uint32_t abort_flag = sm + kAbortAt;
+
+  // ---- before the previous kernel has ended: barriers and TMEM ---------------
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(sm + kFull + 8 * i, 1);
+      bar_init(sm + kEmpty + 8 * i, 2);   // both product warps (or one of them twice)
+    }
+    for (int i = 0; i < 4; ++i) {
+      bar_init(sm + kSFull + 8 * i, 1);
+      bar_init(sm + kPFull + 8 * i, 4);   // the warps of the warpgroup
+      bar_init(sm + kODone + 8 * i, 1);
+    }
+    bar_init(sm + kQFull, 1);
+    bar_init(sm + kQEmpty, 2);
+    for (int i = 0; i < kAhead; ++i) {
+      bar_init(sm + kSegFull + 8 * i, 1);
+      bar_init(sm + kSegEmptied + 8 * i, 11);   // softmax, product and load warps
+    }
+    bar_init(sm + kMeet, kSoftmaxThreads / 32);
+    bar_init(sm + kReady, 1);
+    bar_init(sm + kDrain, 1);
+    bar_init(sm + kDrain + 8, 1);
+    *reinterpret_cast<volatile int*>(smem + kAbortAt) = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(reinterpret_cast<uint32_t*>(smem + kTmemAt), 512);
+  if (tid == kLoadWarp * 32) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_q1);
+  }
   griddep_wait();
   griddep_launch_dependents();
 
-  uint8_t* q_smem = smem + kStages * kStageBytes;
-  float* ml = reinterpret_cast<float*>(q_smem + 2 * kQTileBytes);   // [2 warpgroups][m, l][128 rows]
-  uint64_t* full = reinterpret_cast<uint64_t*>(ml + 2 * 2 * 128);
-  uint64_t* empty = full + kStages;
-  uint64_t* s_full = empty + kStages;   // [2][2]
-  uint64_t* p_full = s_full + 4;        // [2][2]
-  uint64_t* o_done = p_full + 4;        // [2][2], by the score buffer that the product read
-  uint64_t* q_full = o_done + 4;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* drain = q_empty + 1;
-  uint64_t* join = drain + 1;           // all 8 softmax warps
-  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(join + 1);
-  int* flags = reinterpret_cast<int*>(tmem_ptr + 1);   // [0] abort
-
   // ---- the unit list: validity, total, and the place where this CTA starts --
-  // (The scratch of the scan lies in the ring, which is empty until the roles start.)
+  // (The scratch lies in the ring, which is empty until the roles start.)
   int64_t* scan = reinterpret_cast<int64_t*>(smem);
+  List* found = reinterpret_cast<List*>(scan + 40);
   const int V = plan.lists();
   const int per = (V + kThreads - 1) / kThreads;
   const int v_lo = min(V, tid * per), v_hi = min(V, v_lo + per);
-  int bad = (smem_u32(smem) & 1023u) ? 1 : 0;
+  int bad = 0;
   int64_t mine = 0;
   const int n_cu = plan.prefix_mode ? plan.groups : plan.B;
-  if (tid == 0 && n_cu > 0) {
+  if (tid == kThreads - 1 && n_cu > 0) {
     bad |= ld_dep(plan.cu) != 0;
     const int last = ld_dep(plan.cu + n_cu);
     bad |= last < 0 || last > plan.rows;
   }
+  auto units_of_list = [&](const List& s) {
+    return s.nq > 0 ? kNumKVHeads * units_before(plan, s, tiles_of(s)) : 0;
+  };
+  List s_last = {};   // the thread's last list: its only one for up to kThreads lists
   for (int v = v_lo; v < v_hi; ++v) {
-    const List s = load_list(plan, v);
-    if (s.len < 0 && blockIdx.x == 0) set_status(status, LSA_DEV_ERR_BAD_COUNT);
-    bad |= s.nq < 0 || (!plan.prefix_mode && s.nq > plan.max_q);
-    if (s.nq > 0) mine += kNumKVHeads * units_before(plan, s, tiles_of(s));
+    s_last = load_list(plan, v);
+    if (s_last.len < 0 && blockIdx.x == 0) set_status(status, LSA_DEV_ERR_BAD_COUNT);
+    bad |= s_last.nq < 0 || (!plan.prefix_mode && s_last.nq > plan.max_q);
+    mine += units_of_list(s_last);
   }
   int64_t total;
   bad = __syncthreads_or(bad);
   const int64_t before = block_scan<kThreads / 32>(bad ? 0 : mine, scan, &total);
   const Partition part(total, gridDim.x);
   const int64_t u0 = part.start(blockIdx.x), u1 = part.start(blockIdx.x + 1);
-  if (blockIdx.x == 0 && tid == 0) {
-    if (bad) set_status(status, LSA_DEV_ERR_CAPACITY);
-    *work.ok = bad ? 0 : 1;
-    work.base[plan.prefix_mode ? V : 0] = total;
+  if (part.base >= (1 << 30)) bad = 1;   // a CTA counts its units in 32 bits
+  if (sm & 1023u) {                      // the 128-byte swizzle repeats every 1024 bytes
+    if (tid == 0) set_status(status, LSA_DEV_ERR_INTERNAL);
+    bad = 1;
   }
-  if (!bad) {
-    int64_t at = before;
-    const bool here = before <= u0 && u0 < before + mine && u0 < u1;
-    const bool write = plan.prefix_mode && blockIdx.x == 0;
-    if (here || write) {
-      for (int v = v_lo; v < v_hi; ++v) {
-        const List s = load_list(plan, v);
-        const int64_t n = s.nq > 0 ? kNumKVHeads * units_before(plan, s, tiles_of(s)) : 0;
-        if (write) work.base[v] = at;
-        if (here && at <= u0 && u0 < at + n) {
-          scan[32] = v;
-          scan[33] = at;
-        }
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      if (bad) set_status(status, LSA_DEV_ERR_CAPACITY);
+      if (plan.prefix_mode) *work.ok = bad ? 0 : 1;
+    }
+    if (plan.prefix_mode && !bad)   // sequences behind the last group have no prefix
+      for (int x = (n_cu ? ld_dep(plan.cu + n_cu) : 0) * kNumKVHeads + tid; x < plan.B * kNumKVHeads; x += kThreads)
+        work.ends[x] = kNone;
+  }
+  const bool idle = bad || u0 >= u1;
+  if (!idle && before <= u0 && u0 < before + mine) {   // one thread: the list of unit u0
+    int64_t at = before, n = mine;
+    int v = v_lo;
+    if (per > 1) {
+      for (;; ++v) {
+        s_last = load_list(plan, v);
+        n = units_of_list(s_last);
+        if (u0 < at + n) break;
         at += n;
       }
     }
+    *found = s_last;
+    scan[32] = v;
+    scan[33] = u0 - at;
+    scan[34] = n / kNumKVHeads;
   }
-  if (bad || u0 >= u1) {
-    if (!plan.prefix_mode && tid < 4) work.seg[blockIdx.x * 4 + tid] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);   // one arrival per warp of the warpgroup
-      mbar_init(&o_done[i], 1);
-    }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(drain, 1);
-    mbar_init(join, kSoftmaxThreads / 32);
-    flags[0] = 0;
-    mbar_fence_init();
-  }
-  if (warp == kMmaWarp) tmem_alloc(tmem_ptr, 512);
+  fence_proxy_async_smem();   // the scratch was written here; TMA writes it next
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  const uint32_t tmem = *tmem_ptr;
-  volatile int* abort_flag = flags;
-  Cursor cur;
-  cur.start(plan, static_cast<int>(scan[32]), u0 - scan[33]);
-  fence_proxy_async_smem();   // the scan's scratch was written here; TMA writes it next
-  __syncthreads();
-
-  auto give_up = [&]() {
-    if (!*abort_flag) set_status(status, LSA_DEV_ERR_TIMEOUT);
-    *abort_flag = 1;
+  const uint32_t tmem = *reinterpret_cast<const volatile uint32_t*>(smem + kTmemAt);
+  const Seg* const segs = reinterpret_cast<const Seg*>(smem + kSegAt);
+  auto wait = [&](int bar, unsigned parity) { return bar_wait(sm + bar, parity, abort_flag, status); };
+  // Segment k of this CTA; its place is free again once every role has said so.
+  auto seg_get = [&](unsigned k) { return wait(kSegFull + 8 * (k % kAhead), (k / kAhead) & 1); };
+  auto seg_done = [&](unsigned k) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(sm + kSegEmptied + 8 * (k % kAhead));
   };
 
-  if (warp == kLoadWarp) {
-    // ============================ K and V of the units =======================
-    uint64_t policy_once = 0, policy_again = 0;
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      policy_once = l2_policy_evict_first();
-      policy_again = l2_policy_evict_normal();
-    }
-    const int beyond = static_cast<int>(plan.n_slots) * (kNumKVHeads * kChunkTokens);   // reads as zeros
-    int64_t it = 0;
-    bool ok = true;
-    for (int64_t u = u0; ok;) {
-      const int j1 = static_cast<int>(min(static_cast<int64_t>(cur.n), cur.j + (u1 - u)));
-      // Another tile of the list reads the same chunks: they stay in L2.
-      const uint64_t policy = cur.tiles > 1 ? policy_again : policy_once;
-      int row = 0;
-      for (int j = cur.j; j < j1; ++j, ++it) {
-        if (((j - cur.j) & 31) == 0) {   // the rows of 32 units at a time, a lane each
-          row = beyond;
-          if (!cur.empty && j + lane < j1) {
-            const int c = cur.chunk(j + lane);
-            const int64_t slot = cur.s.table ? ld_dep(cur.s.table + c) : cur.s.ident + c;
-            if (slot >= 0 && slot < plan.n_slots)
-              row = (static_cast<int>(slot) * kNumKVHeads + cur.g) * kChunkTokens;
-            else
-              set_status(status, LSA_DEV_ERR_BAD_SLOT);
-          }
-        }
-        const int y = __shfl_sync(0xffffffffu, row, (j - cur.j) & 31);
-        const int st = static_cast<int>(it % kStages);
-        int good = 1;
-        if (lane == 0) {
-          if (it >= kStages) good = mbar_wait_bounded(&empty[st], static_cast<unsigned>((it / kStages - 1) & 1), abort_flag);
-          if (good) {
-            uint8_t* dst = smem + st * kStageBytes;
-            mbar_arrive_expect_tx(&full[st], kStageBytes);
-            tma_load_2d(dst, &tm_k, 0, y, &full[st], policy);
-            tma_load_2d(dst + kBoxBytes, &tm_k, 64, y, &full[st], policy);
-            tma_load_2d(dst + 2 * kBoxBytes, &tm_v, 0, y, &full[st], policy);
-            tma_load_2d(dst + 3 * kBoxBytes, &tm_v, 64, y, &full[st], policy);
-          } else {
-            give_up();
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-        if (!ok) break;
+  if (warp >= kMmaWarp) {
+    fewer_registers<kOtherRegs>();
+    if (warp == kPlanWarp) {
+      // ===================== the list, and the query tiles ===================
+      Cursor cur = {};
+      int left = 0;
+      if (!idle) {
+        cur.start(plan, static_cast<int>(scan[32]), *found, scan[34], scan[33]);
+        left = static_cast<int>(u1 - u0);
       }
-      u += j1 - cur.j;
-      if (u >= u1) break;
-      if (ok) cur.next(plan);
-    }
-    if (lane == 0 && *abort_flag) {   // copies in flight land before the CTA ends
-      int never = 0;
-      for (int64_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-        mbar_wait_bounded(&full[i % kStages], static_cast<unsigned>((i / kStages) & 1), &never);
-    }
-  } else if (warp == kQueryWarp) {
-    // ================================ query tiles =============================
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_q1);
-      unsigned segs = 0;
-      for (int64_t u = u0;;) {
-        const int j1 = static_cast<int>(min(static_cast<int64_t>(cur.n), cur.j + (u1 - u)));
-        if (segs && !mbar_wait_bounded(q_empty, (segs - 1) & 1, abort_flag)) {
-          give_up();
-          break;
-        }
-        const int row = cur.s.q0 + cur.t * kWideQ, head = cur.g * kGroup;
-        if (cur.cnt == 1) {   // 8 rows; what the other rows of the tile hold is not read back
-          mbar_arrive_expect_tx(q_full, 2 * kGroup * 128);
-          tma_load_3d(q_smem, &tm_q1, 0, head, row, q_full);
-          tma_load_3d(q_smem + kQBoxBytes, &tm_q1, 64, head, row, q_full);
+      __syncwarp();
+      if (lane == 0) bar_arrive(sm + kReady);   // the scratch has been read: the ring may be filled
+      const int me = blockIdx.x;
+      int4 seg0 = make_int4(0, 0, 0, 0), seg1 = seg0;
+      unsigned put = 0;      // segments written
+      bool ended = false;    // the list's end is
+      auto publish = [&]() {
+        if (put >= kAhead && !wait(kSegEmptied + 8 * (put % kAhead), (put / kAhead - 1) & 1)) return false;
+        Seg* const s = reinterpret_cast<Seg*>(smem + kSegAt) + put % kAhead;
+        if (left <= 0) {
+          if (lane == 0) s->units = 0;
+          ended = true;
         } else {
-          const int halves = cur.wide() ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, halves * kQTileBytes);
-          for (int w = 0; w < halves; ++w) {
-            tma_load_3d(q_smem + w * kQTileBytes, &tm_q, 0, head, row + w * kHalfQ, q_full);
-            tma_load_3d(q_smem + w * kQTileBytes + kQBoxBytes, &tm_q, 64, head, row + w * kHalfQ, q_full);
+          const int units = min(cur.n - cur.j, left), row = cur.s.q0 + cur.t * kWideQ;
+          const bool begins = cur.j == 0, ends = cur.j + units == cur.n;
+          if (lane == 0) {
+            s->units = units;
+            s->flags = (cur.cnt > kHalfQ ? kSegWide : 0) | (cur.empty ? kSegEmpty : 0) | (cur.tiles > 1 ? kSegAgain : 0) |
+                       (plan.prefix_mode && cur.v < plan.groups ? kSegGroup : 0) | (begins && ends ? kSegWhole : 0);
+            s->j0 = cur.j;
+            s->cnt = cur.cnt;
+            s->row = row;
+            s->head = cur.g * kGroup;
+            s->first = cur.first;
+            s->low = cur.low;
+            int f0 = 0, f1 = 0, f2 = -1;
+            if (plan.prefix_mode) {
+              f0 = cur.s.len / kChunkTokens;
+            } else if (!cur.empty) {
+              f0 = min(cur.first, plan.sinks / kChunkTokens);
+              f1 = cur.first + (max(0, cur.p0 + cur.cnt - plan.window + kChunkTokens - 1) >> 6) - cur.low;
+              f2 = cur.first + ((cur.p0 - (kChunkTokens - 1)) >> 6) - cur.low;
+            }
+            s->f0 = f0;
+            s->f1 = f1;
+            s->f2 = f2;
+            s->p0 = cur.p0;
+            s->len = cur.s.len;
+            s->g = cur.g;
+            s->table = cur.s.table;
+            s->ident = cur.s.ident;
+          }
+          // What the merge has to know.
+          if (plan.prefix_mode) {
+            if (lane < cur.cnt) {
+              int* at = work.ends + (cur.v < plan.groups ? 0 : 2 * kNumKVHeads * plan.B) + (row + lane) * kNumKVHeads + cur.g;
+              if (begins) at[0] = me | (put ? kEndSlot : 0) | (lane << kEndPlace) | (ends ? kEndWhole : 0);
+              if (ends) at[kNumKVHeads * plan.B] = me;
+            }
+          } else if (!(begins && ends)) {
+            const int64_t tile_u = u1 - left - cur.j;   // the tile's first unit
+            const int lo = begins ? me : part.cta_of(tile_u), hi = ends ? me : part.cta_of(tile_u + cur.n - 1);
+            const int4 a = make_int4(row, cur.g | (cur.cnt << 8), lo | (hi << 16), 2 * lo + (part.start(lo) == tile_u ? 0 : 1) + 1);
+            if (put) seg1 = a;
+            else seg0 = a;
+          }
+          left -= units;
+          if (left > 0) cur.next(plan);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(sm + kSegFull + 8 * (put % kAhead));
+        ++put;
+        return true;
+      };
+      bool ok = true;
+      unsigned loads = 0;
+      // One place stays free: in segment k the planner writes segment k + 7 where
+      // k - 1 was, which does not hold back the query tile of k + 1.
+      for (int i = 0; ok && i < kAhead - 1 && !ended; ++i) ok = publish();
+      for (unsigned k = 0; ok; ++k) {
+        const Seg& s = segs[k % kAhead];
+        const int units = s.units, cnt = s.cnt, row = s.row, head = s.head;
+        if (units == 0) break;
+        if (k) ok = wait(kQEmpty, (k - 1) & 1);
+        if (!ok) break;
+        ++loads;
+        if (lane == 0) {
+          const uint32_t bar = sm + kQFull, q = sm + kQAt;
+          if (cnt == 1) {   // 8 rows; what the other rows of the tile hold is not read back
+            bar_expect(bar, 2 * kGroup * 128);
+            load_box(q, &tm_q1, 0, head, row, bar);
+            load_box(q + kQBoxBytes, &tm_q1, 64, head, row, bar);
+          } else {
+            const int halves = cnt > kHalfQ ? 2 : 1;
+            bar_expect(bar, halves * kQTileBytes);
+            for (int w = 0; w < halves; ++w) {
+              load_box(q + w * kQTileBytes, &tm_q, 0, head, row + w * kHalfQ, bar);
+              load_box(q + w * kQTileBytes + kQBoxBytes, &tm_q, 64, head, row + w * kHalfQ, bar);
+            }
           }
         }
-        ++segs;
-        u += j1 - cur.j;
-        if (u >= u1) break;
-        cur.next(plan);
+        __syncwarp();
+        if (!ended) ok = publish();
       }
-      if (*abort_flag && segs) {
-        int never = 0;
-        mbar_wait_bounded(q_full, (segs - 1) & 1, &never);
+      if (!plan.prefix_mode && lane < 2) work.seg[2 * me + lane] = lane ? seg1 : seg0;
+      if (!ok && lane == 0 && loads) {   // a tile in flight lands before the CTA ends
+        volatile int never = 0;
+        mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kQFull), (loads - 1) & 1, &never);
       }
-    }
-  } else if (warp == kMmaWarp) {
-    // ================================= products ===============================
-    if (lane == 0) {
-      const uint32_t ring = smem_u32(smem), q_base = smem_u32(q_smem);
-      int64_t it = 0;
-      unsigned jobs[2] = {0, 0};   // units each warpgroup has had
-      unsigned segs = 0;
-      bool ok = true;
-      for (int64_t u = u0; ok;) {
-        const int j1 = static_cast<int>(min(static_cast<int64_t>(cur.n), cur.j + (u1 - u)));
-        const int n = j1 - cur.j;
-        const bool wide = cur.wide();
-        const int ahead = wide ? 2 : 4;   // both score buffers of both warpgroups
-        ok = mbar_wait_bounded(q_full, segs & 1, abort_flag);
-        // S of unit i, into the score buffer that O(job - 2) has read.
-        auto scores = [&](int i) {
-          const int st = static_cast<int>((it + i) % kStages);
-          if (!mbar_wait_bounded(&full[st], static_cast<unsigned>(((it + i) / kStages) & 1), abort_flag)) return false;
-          tcgen05_fence_after();
-          const uint32_t kb = ring + st * kStageBytes;
-          for (int w = wide ? 0 : (i & 1); w < (wide ? 2 : (i & 1) + 1); ++w) {
-            const unsigned job = jobs[w] + (wide ? i : i >> 1);
-            const int buf = 2 * w + (job & 1);
-            if (job >= 2 && !mbar_wait_bounded(&o_done[buf], ((job - 2) >> 1) & 1, abort_flag)) return false;
-            const uint32_t qa = q_base + (wide ? w * kQTileBytes : 0);
-            const uint32_t d = tmem + buf * kSCols;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_bf16(d, umma_desc_kmajor_sw128(qa + (k >> 2) * kQBoxBytes + (k & 3) * 32),
-                        umma_desc_kmajor_sw128(kb + (k >> 2) * kBoxBytes + (k & 3) * 32), kIdescS, k > 0);
-            umma_commit(&s_full[buf]);
+    } else if (warp == kLoadWarp) {
+      // ========================== K and V of the units =======================
+      const uint64_t policy_once = l2_policy_evict_first(), policy_again = l2_policy_evict_normal();
+      const int beyond = static_cast<int>(plan.n_slots) * (kNumKVHeads * kChunkTokens);   // reads as zeros
+      unsigned it = 0;
+      bool ok = wait(kReady, 0);
+      for (unsigned k = 0; ok; ++k) {
+        ok = seg_get(k);
+        if (!ok) break;
+        const Seg& s = segs[k % kAhead];
+        const int units = s.units, flags = s.flags, j0 = s.j0, first = s.first, low = s.low, g = s.g;
+        const int32_t* const table = s.table;
+        const int64_t ident = s.ident;
+        seg_done(k);
+        if (units == 0) break;
+        // Another tile of the list reads the same chunks: they stay in L2.
+        const uint64_t policy = (flags & kSegAgain) ? policy_again : policy_once;
+        int row = 0;
+        for (int i = 0; i < units; ++i, ++it) {
+          if ((i & 31) == 0) {   // the rows of 32 units at a time, a lane each
+            row = beyond;
+            if (!(flags & kSegEmpty) && i + lane < units) {
+              const int j = j0 + i + lane, c = j < first ? j : low + j - first;
+              const int64_t slot = table ? ld_dep(table + c) : ident + c;
+              if (slot >= 0 && slot < plan.n_slots)
+                row = (static_cast<int>(slot) * kNumKVHeads + g) * kChunkTokens;
+              else
+                set_status(status, LSA_DEV_ERR_BAD_SLOT);
+            }
           }
-          if (i == n - 1) umma_commit(q_empty);
-          return true;
-        };
-        for (int i = 0; ok && i < min(ahead, n); ++i) ok = scores(i);
-        for (int i = 0; ok && i < n; ++i) {
-          const int st = static_cast<int>((it + i) % kStages);
-          const uint32_t vb = ring + st * kStageBytes + 2 * kBoxBytes;
-          for (int w = wide ? 0 : (i & 1); ok && w < (wide ? 2 : (i & 1) + 1); ++w) {
-            const unsigned done = wide ? i : i >> 1;
-            const unsigned job = jobs[w] + done;
-            const int buf = 2 * w + (job & 1);
-            ok = mbar_wait_bounded(&p_full[buf], (job >> 1) & 1, abort_flag);
+          const int y = __shfl_sync(0xffffffffu, row, i & 31);
+          const int st = it % kStages;
+          if (it >= kStages) ok = wait(kEmpty + 8 * st, (it / kStages - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t dst = sm + st * kStageBytes, bar = sm + kFull + 8 * st;
+            bar_expect(bar, kStageBytes);
+            load_box(dst, &tm_k, 0, y, bar, policy);
+            load_box(dst + kBoxBytes, &tm_k, 64, y, bar, policy);
+            load_box(dst + 2 * kBoxBytes, &tm_v, 0, y, bar, policy);
+            load_box(dst + 3 * kBoxBytes, &tm_v, 64, y, bar, policy);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) {   // copies in flight land before the CTA ends
+        volatile int never = 0;
+        for (unsigned i = it > kStages ? it - kStages : 0; i < it; ++i)
+          mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kFull) + i % kStages, (i / kStages) & 1, &never);
+      }
+    } else {
+      // =============================== products ==============================
+      // A warp for each softmax warpgroup: the issue of one's products, and its
+      // waits, run beside the other's.  The whole warp walks the segments (its
+      // values stay uniform) and one lane issues.
+      const int w = warp - kMmaWarp;
+      const uint32_t leader = elect_one() ? 1u : 0u;
+      const uint32_t k_lo0 = desc_lo_kmajor(sm), v_lo0 = desc_lo_v(sm + 2 * kBoxBytes), q_lo0 = desc_lo_kmajor(sm + kQAt);
+      const uint32_t o_acc = tmem + kOCol0 + w * kHeadDim, s_col0 = tmem + 2 * w * kSCols;
+      const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
+      unsigned it = 0, job = 0;   // units, and units of this warpgroup so far
+      bool ok = true;
+      for (unsigned k = 0; ok; ++k) {
+        ok = seg_get(k);
+        if (!ok) break;
+        const int n = segs[k % kAhead].units;
+        const bool wide = segs[k % kAhead].flags & kSegWide;
+        seg_done(k);
+        if (n == 0) break;
+        const int mine = wide ? n : (n + 1 - w) >> 1;   // units of this warpgroup: all, or every other one
+        const unsigned step = wide ? 1 : 2, at0 = it + (wide ? 0 : w);
+        const uint32_t q_lo = q_lo0 + (wide ? w * (kQTileBytes >> 4) : 0);
+        ok = wait(kQFull, k & 1);
+        if (ok && !mine && lane == 0) bar_arrive(sm + kQEmpty);
+        // Scores run up to two units (both buffers) before the products, as far
+        // as units have arrived: waiting for one that has not would hold back the
+        // product that frees a stage.
+        int next = 0;
+        for (int i = 0; ok && i < mine; ++i) {
+          for (; next < min(mine, i + 2); ++next) {
+            const unsigned at = at0 + next * step, st = at % kStages, x = job + next, buf = x & 1;
+            if (next > i) {
+              if (!__all_sync(0xffffffffu, bar_try(sm + kFull + 8 * st, (at / kStages) & 1))) break;
+            } else {
+              ok = wait(kFull + 8 * st, (at / kStages) & 1);
+            }
+            if (ok && x >= 2) ok = wait(o_bar + 8 * buf, ((x - 2) >> 1) & 1);   // the buffer's probabilities are read
             if (!ok) break;
             tcgen05_fence_after();
+            const uint32_t k_lo = k_lo0 + st * (kStageBytes >> 4), d = s_col0 + buf * kSCols;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16_ts(tmem + kOCol0 + w * kHeadDim, tmem + buf * kSCols + 8 * k,
-                           umma_desc_v(vb + k * 2048), kIdescO, done > 0 || k > 0);
-            umma_commit(&o_done[buf]);
+            for (int x8 = 0; x8 < 8; ++x8)
+              mma_ss(leader, d, q_lo + (x8 >> 2) * (kQBoxBytes >> 4) + (x8 & 3) * 2,
+                     k_lo + (x8 >> 2) * (kBoxBytes >> 4) + (x8 & 3) * 2, kIdescS, x8 > 0);
+            mma_commit(leader, sm + s_bar + 8 * buf);
+            if (next == mine - 1) mma_commit(leader, sm + kQEmpty);
           }
           if (!ok) break;
-          umma_commit(&empty[st]);
-          if (i + ahead < n) ok = scores(i + ahead);
+          const unsigned at = at0 + i * step, st = at % kStages, x = job + i, buf = x & 1;
+          ok = wait(p_bar + 8 * buf, (x >> 1) & 1);
+          if (!ok) break;
+          tcgen05_fence_after();
+          const uint32_t v_lo = v_lo0 + st * (kStageBytes >> 4), a = s_col0 + buf * kSCols;
+#pragma unroll
+          for (int x4 = 0; x4 < 4; ++x4)
+            mma_ts(leader, o_acc, a + 8 * x4, v_lo + x4 * (2048 >> 4), kIdescO, x4 > 0 || i > 0);
+          mma_commit(leader, sm + o_bar + 8 * buf);
+          mma_commit(leader, sm + kEmpty + 8 * st);
+          if (!wide) mma_commit(leader, sm + kEmpty + 8 * st);
         }
-        if (!ok) break;
-        jobs[0] += wide ? n : (n + 1) >> 1;
-        jobs[1] += wide ? n : n >> 1;
+        job += mine;
         it += n;
-        ++segs;
-        u += n;
-        if (u >= u1) break;
-        cur.next(plan);
       }
-      if (!ok) give_up();
-      umma_commit(drain);   // every product has ended before TMEM is given back
-      int never = 0;
-      mbar_wait_bounded(drain, 0, &never);
+      mma_commit(leader, sm + kDrain + 8 * w);   // every product has ended before TMEM is given back
+      volatile int never = 0;
+      mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kDrain) + w, 0, &never);
     }
   } else {
     // ================================= softmax ================================
+    more_registers<kSoftmaxRegs>();
     const int w = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;                    // row of the tile
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t o_mine = tmem + kOCol0 + w * kHeadDim + lanes;
-    unsigned jobs[2] = {0, 0};
-    int64_t it = 0;
+    const uint32_t s_col0 = tmem + 2 * w * kSCols + lanes, o_mine = tmem + kOCol0 + w * kHeadDim + lanes;
+    const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
+    const uint64_t scale2 = pack2(scale_log2, scale_log2);
+    unsigned job0 = 0, job1 = 0, it = 0, joins = 0;
     bool ok = true;
-    int seg_no = 0;
-    unsigned joins = 0;
-    // The same answer in every lane: the warp's collective instructions stay whole.
-    auto warp_wait = [&](uint64_t* bar, unsigned parity) {
-      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag)) != 0;
-    };
-    // Both warpgroups, with a bounded wait.
+    // Both warpgroups.
     auto meet = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(join);
-      return warp_wait(join, joins++ & 1);
+      if (lane == 0) bar_arrive(sm + kMeet);
+      return wait(kMeet, joins++ & 1);
     };
-    for (int64_t u = u0; ok; ++seg_no) {
-      const int j0 = cur.j;
-      const int j1 = static_cast<int>(min(static_cast<int64_t>(cur.n), j0 + (u1 - u)));
-      const int n = j1 - j0;
-      const bool wide = cur.wide();
-      const int rows = kGroup * (wide ? (w == 0 ? kHalfQ : cur.cnt - kHalfQ) : cur.cnt);   // of this warpgroup
+    for (unsigned k = 0; ok; ++k) {
+      ok = seg_get(k);
+      if (!ok) break;
+      const Seg& sg = segs[k % kAhead];
+      const int n = sg.units, j0 = sg.j0, f0 = sg.f0 - j0, f1 = sg.f1 - j0, f2 = sg.f2 - j0;
+      if (n == 0) break;
+      const bool wide = sg.flags & kSegWide;
+      const int rows = kGroup * (wide ? (w == 0 ? kHalfQ : sg.cnt - kHalfQ) : sg.cnt);   // of this warpgroup
       const bool active = wq * 32 < rows;            // the warp has rows
-      const int i_q = (wide ? w * kHalfQ : 0) + (r >> 3);   // query of the tile
-      const int pos = cur.p0 + i_q;
       float m = -INFINITY, l = 0.f;
-      unsigned job = jobs[w];
+      const unsigned job_first = w ? job1 : job0;
+      unsigned job = job_first;
       for (int i = wide ? 0 : w; i < n; i += wide ? 1 : 2, ++job) {
-        const int buf = 2 * w + (job & 1);
-        if (!warp_wait(&s_full[buf], (job >> 1) & 1)) {
-          give_up();
-          ok = false;
-          break;
-        }
+        const unsigned buf = job & 1;
+        uint64_t see = ~0ull;                        // tokens of the unit that this row sees
+        const bool edge = !(i < f0 || (i >= f1 && i <= f2));
+        ok = wait(s_bar + 8 * buf, (job >> 1) & 1);
+        if (!ok) break;
         tcgen05_fence_after();
-        // Rows of this unit that some query of the tile sees.
-        const int kb = (cur.empty ? 0 : cur.chunk(j0 + i)) * kChunkTokens;
-        const int p1 = cur.p0 + cur.cnt - 1;
-        int last, low;                               // seen by all: [low, last] relative to the unit
-        uint64_t any;
-        bool edge;
-        if (plan.prefix_mode) {
-          last = cur.s.len - 1 - kb;                 // len -1 (invalid) or 0: nothing
-          low = 0;
-          any = lowest(last + 1);
-          edge = last < 63;
-        } else {
-          any = cur.empty ? 0ull
-                          : lowest(p1 - kb + 1) & (~lowest(cur.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
-          edge = cur.p0 - kb < 63 || (p1 - plan.window + 1 - kb > 0 && plan.sinks - kb < 64);
-          last = pos - kb;
-          low = pos - plan.window + 1 - kb;
-        }
-        if (any != ~0ull) {
-          // Unseen rows of V become zeros (their probabilities are zero, what
-          // the page holds there may not be finite).  Both warpgroups of a wide
-          // tile write the same zeros.
-          const int64_t unit = it + i;
-          const int st = static_cast<int>(unit % kStages);
-          if (!warp_wait(&full[st], static_cast<unsigned>((unit / kStages) & 1))) {
-            give_up();
-            ok = false;
-            break;
+        if (edge) {
+          uint64_t any;                              // tokens that some query of the tile sees
+          const int j = j0 + i, kb = (j < sg.first ? j : sg.low + j - sg.first) * kChunkTokens;
+          if (sg.flags & kSegEmpty) {
+            any = see = 0;
+          } else if (plan.prefix_mode) {
+            any = see = lowest(sg.len - kb);
+          } else {
+            const int pos = sg.p0 + (wide ? w * kHalfQ : 0) + (r >> 3) - kb;   // of the row's query, in the unit
+            any = lowest(sg.p0 + sg.cnt - kb) & (~lowest(sg.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
+            see = lowest(pos + 1) & (~lowest(pos - plan.window + 1) | lowest(plan.sinks - kb));
           }
-          uint8_t* vs = smem + st * kStageBytes + 2 * kBoxBytes;
-          for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
-            const int row = x >> 4;
-            if (!((any >> row) & 1))
-              *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          if (any != ~0ull) {
+            // Unseen rows of V become zeros (their probabilities are zero, what
+            // the page holds there may not be finite).  Both warpgroups of a wide
+            // tile write the same zeros.
+            const unsigned at = it + i, st = at % kStages;
+            ok = wait(kFull + 8 * st, (at / kStages) & 1);
+            if (!ok) break;
+            uint8_t* vs = smem + st * kStageBytes + 2 * kBoxBytes;
+            for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
+              const int row = x >> 4;
+              if (!((any >> row) & 1))
+                *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
         }
         if (active) {
-          const uint32_t sp = tmem + buf * kSCols + lanes;
+          const uint32_t sp = s_col0 + buf * kSCols;
           float s[64];
           tmem_ld32(sp, s);
           tmem_ld32(sp + 32, s + 32);
           tmem_wait_ld(s, 64);
           if (edge) {
-            const uint64_t see = plan.prefix_mode || cur.empty
-                                     ? any
-                                     : lowest(last + 1) & (~lowest(low) | lowest(plan.sinks - kb));
-            const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
+            const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              if (!((s0 >> c) & 1)) s[c] = -INFINITY;
-              if (!((s1 >> c) & 1)) s[c + 32] = -INFINITY;
+              if (!((see0 >> c) & 1)) s[c] = -INFINITY;
+              if (!((see1 >> c) & 1)) s[c + 32] = -INFINITY;
             }
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
 #pragma unroll
-          for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-          const bool raise = top > m + kRaise;       // the first finite score always does
+          for (int c = 12; c < 60; c += 8) {
+            mx[0] = max3(mx[0], s[c], s[c + 1]);
+            mx[1] = max3(mx[1], s[c + 2], s[c + 3]);
+            mx[2] = max3(mx[2], s[c + 4], s[c + 5]);
+            mx[3] = max3(mx[3], s[c + 6], s[c + 7]);
+          }
+          mx[0] = max3(mx[0], s[60], s[61]);
+          mx[1] = max3(mx[1], s[62], s[63]);
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale_log2;
+          const bool raise = top > m + kRaise && r < rows;   // a row's first finite score always does
           if (__any_sync(0xffffffffu, raise)) {
             const float m_new = raise ? top : m;
             const float f = raise ? fast_exp2(m - m_new) : 1.f;
             m = m_new;
             l *= f;
-            if (job != jobs[w]) {                    // the accumulator of earlier units follows
-              if (!warp_wait(&o_done[2 * w + ((job - 1) & 1)], ((job - 1) >> 1) & 1)) {
-                give_up();
-                ok = false;
-              }
+            if (job != job_first) {                  // the accumulator of earlier units follows
+              ok = wait(o_bar + 8 * (buf ^ 1), ((job - 1) >> 1) & 1);
+              if (!ok) break;
               tcgen05_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < kHeadDim; c += 32) {
                 float o[32];
                 tmem_ld32(o_mine + c, o);
@@ -714,132 +941,134 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every probability is 0
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t ref2 = pack2(-ref, -ref);
+          uint64_t sum[4] = {0, 0, 0, 0};
           float pk[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float a = fast_exp2(fmaf(s[2 * c], scale_log2, -ref)), b = fast_exp2(fmaf(s[2 * c + 1], scale_log2, -ref));
-            sum[c & 3] += a + b;
+            float a, b;
+            unpack2(fma2(pack2(s[2 * c], s[2 * c + 1]), scale2, ref2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum[c & 3] = add2(sum[c & 3], pack2(a, b));
             // One rounding of the probabilities to bf16, half a step (2^-9) at
             // most: the output is rounded to the same type.
             pk[c] = __uint_as_float(pack_bf16(a, b));
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_st32(sp, pk);
+          float sa, sb;
+          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), sa, sb);
+          l += sa + sb;
           tmem_wait_st();
         }
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
-        if (!ok) break;
+        if (lane == 0) bar_arrive(sm + p_bar + 8 * buf);
       }
       if (!ok) break;
 
       // ---- the end of a segment: the tile's output, or this CTA's partial ----
       const unsigned n0 = wide ? n : (n + 1) >> 1, n1 = wide ? n : n >> 1;
-      const bool whole = !plan.prefix_mode && j0 == 0 && j1 == cur.n;
-      const unsigned had = w == 0 ? n0 : n1;
-      const unsigned last0 = jobs[0] + n0 - 1, last1 = jobs[1] + n1 - 1;
+      const unsigned last0 = job0 + n0 - 1, last1 = job1 + n1 - 1;
+      float* const ml = reinterpret_cast<float*>(smem + kMlAt);   // [2 warpgroups][m, l][128 rows]
       if (!wide) {
-        ml[(2 * w + 0) * 128 + r] = had ? m : -INFINITY;
-        ml[(2 * w + 1) * 128 + r] = had ? l : 0.f;
+        ml[2 * w * 128 + r] = m;
+        ml[(2 * w + 1) * 128 + r] = l;
         ok = meet();   // both have their last scores: the waits below name each barrier's next phase
       }
       // The last product of a warpgroup (its commit follows all earlier ones).
-      if (ok && (!wide || w == 0)) ok = warp_wait(&o_done[last0 & 1], (last0 >> 1) & 1);
-      if (ok && (wide ? w == 1 : n1 > 0)) ok = warp_wait(&o_done[2 + (last1 & 1)], (last1 >> 1) & 1);
-      if (!ok) {
-        give_up();
-        break;
-      }
+      if (ok && (!wide || w == 0)) ok = wait(kODone + 8 * (last0 & 1), (last0 >> 1) & 1);
+      if (ok && (wide ? w == 1 : n1 > 0)) ok = wait(kODone + 16 + 8 * (last1 & 1), (last1 >> 1) & 1);
+      if (!ok) break;
       tcgen05_fence_after();
-      float f0 = 1.f, f1 = 0.f;
+      float part0 = 1.f, part1 = 0.f;
       if (!wide) {
         const float m0 = ml[r], l0 = ml[128 + r], m1 = ml[256 + r], l1 = ml[384 + r];
         m = fmaxf(m0, m1);
         const float ref = m == -INFINITY ? 0.f : m;
-        f0 = fast_exp2(m0 - ref);
-        f1 = fast_exp2(m1 - ref);
-        l = l0 * f0 + l1 * f1;
+        part0 = fast_exp2(m0 - ref);
+        part1 = fast_exp2(m1 - ref);
+        l = l0 * part0 + l1 * part1;
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      f0 *= inv;
-      f1 *= inv;
-      // Where the row goes.
-      const int64_t q_row = cur.s.q0 + cur.t * kWideQ + i_q;
-      const int h = r & 7;
-      const bool row_here = r < rows;
-      int64_t rec = 0;
-      if (plan.prefix_mode) {
-        const int64_t tile_row = cur.v < plan.groups
-                                     ? static_cast<int64_t>(kGroup) * (8ll * cur.s.q0 + cur.g * static_cast<int64_t>(cur.s.nq) + cur.t * kWideQ)
-                                     : 64ll * plan.B + 64ll * cur.s.q0 + 8 * cur.g;
-        rec = tile_row + static_cast<int64_t>(blockIdx.x) * work.rows_cap;
-      } else {
-        rec = (2ll * blockIdx.x + (seg_no > 0)) * work.rows_cap;
-      }
-      rec += i_q * kGroup + h;
+      part0 *= inv;
+      part1 *= inv;
+      // Where the rows go: 128 bytes of a row per 8 lanes.  A thread holds a row,
+      // so the rows turn in the warp's 4 KiB of shared memory, 16-byte piece x of
+      // row y at place x ^ (y % 8) (no bank conflicts either way).
       if (active) {
-        const uint32_t o0 = tmem + kOCol0 + lanes, o1 = o0 + kHeadDim;
+        const bool whole = sg.flags & kSegWhole, final = whole && !plan.prefix_mode;
+        const int q_first = (wide ? w * kHalfQ : 0) + wq * 4;   // the warp's first query in the tile
+        // Output rows: (query, head); a record's: the same, a tile at a time.
+        const int64_t out_row = (static_cast<int64_t>(sg.row) + q_first) * kNumQHeads + sg.head;
+        int64_t rec = out_row;
+        int q_rows = kNumQHeads;                                // rows from a query to the next
+        if (plan.prefix_mode && whole) {
+          rec += (sg.flags & kSegGroup) ? 0 : static_cast<int64_t>(kNumQHeads) * plan.B;
+        } else if (!final) {
+          rec = (plan.prefix_mode ? 2ll * kNumQHeads * plan.B : 0) + (2ll * blockIdx.x + (k > 0)) * work.rows_cap +
+                q_first * kGroup;
+          q_rows = kGroup;
+        }
+        uint8_t* const mine = smem + kTurnAt + warp * kTurnBytes;
+        uint8_t* const row_at = mine + lane * 128;
+        // fp32 records go 32 columns at a time, bf16 outputs 64.
         const int c_lo = wide ? 0 : 64 * w, c_hi = wide ? kHeadDim : 64 * w + 64;
+        uint8_t* to = final ? reinterpret_cast<uint8_t*>(out) + (out_row * kHeadDim + c_lo) * 2
+                            : reinterpret_cast<uint8_t*>(work.o + rec * kHeadDim + c_lo);
+        const int row_bytes = final ? 2 * kHeadDim : 4 * kHeadDim;
+#pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
           float o[32];
-          tmem_ld32((wide ? o_mine : o0) + c, o);
-          tmem_wait_ld(o, 32);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] *= f0;
+          tmem_ld32((wide ? o_mine : tmem + kOCol0 + lanes) + c, o);
           if (!wide && n1) {
             float o2[32];
-            tmem_ld32(o1 + c, o2);
+            tmem_ld32(tmem + kOCol0 + kHeadDim + lanes + c, o2);
+            tmem_wait_ld(o, 32);
             tmem_wait_ld(o2, 32);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = fmaf(o2[x], f1, o[x]);
-          }
-          if (row_here) {
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(out + (q_row * kNumQHeads + cur.g * kGroup + h) * kHeadDim + c);
+            for (int x = 0; x < 32; ++x) o[x] = fmaf(o2[x], part1, o[x] * part0);
+          } else {
+            tmem_wait_ld(o, 32);
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                dst[x] = make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                                    pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(work.o + rec * kHeadDim + c);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-            }
+            for (int x = 0; x < 32; ++x) o[x] *= part0;
           }
+          if (final) {
+            const int z = (c >> 3) & 4;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                             pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
+            if (!z) continue;
+          } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4*>(row_at + ((x ^ (lane & 7)) << 4)) =
+                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int y = 4 * x + (lane >> 3);   // row of the warp: query y / 8, head y % 8
+            if (wq * 32 + y < rows)
+              *reinterpret_cast<uint4*>(to + ((y >> 3) * q_rows + (y & 7)) * row_bytes + (lane & 7) * 16) =
+                  *reinterpret_cast<const uint4*>(mine + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+          }
+          __syncwarp();
+          to += 128;
         }
-        if (row_here && !whole && (wide || w == 0)) work.lse[rec] = l == 0.f ? -INFINITY : m + __log2f(l);
-      }
-      // What the merge needs of the CTA's first and last segment.
-      if (!plan.prefix_mode && tid == 0) {
-        const int64_t tile_u = u - j0;   // first unit of the tile
-        const int4 a = make_int4(static_cast<int>(tile_u & 0xffffffff), static_cast<int>(tile_u >> 32), cur.n, cur.cnt);
-        const int4 b = make_int4(cur.s.q0 + cur.t * kWideQ, cur.g, 1, 0);
-        int4* dst = work.seg + blockIdx.x * 4;
-        if (seg_no == 0) {
-          dst[0] = a;
-          dst[1] = b;
-          dst[2] = dst[3] = make_int4(0, 0, 0, 0);
-        } else {
-          dst[2] = a;
-          dst[3] = b;
-        }
+        if (!final && r < rows && (wide || w == 0))
+          work.lse[rec + (lane >> 3) * q_rows + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
       }
       tcgen05_fence_before();
       // In a narrow tile each warpgroup reads the other's accumulator: neither
       // lets the next segment's products start before both have.
-      if (!wide && ok) ok = meet();
-      if (!ok) {
-        give_up();
-        break;
-      }
-      jobs[0] += n0;
-      jobs[1] += n1;
+      if (!wide) ok = meet();
+      seg_done(k);
+      job0 += n0;
+      job1 += n1;
       it += n;
-      u += n;
-      if (u >= u1) break;
-      cur.next(plan);
     }
   }
   __syncwarp();
@@ -855,34 +1084,44 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 
-// The records of one row, in the order of its partials: `row(i)` for i < n.
+// The partials of one row, joined in their order: `row(i)` for i < n.  The loads
+// of 8 partials are issued together.
 struct Fold {
   float m = -INFINITY, den = 0.f;
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
   template <typename Row>
   __device__ void add(const Work& w, int n, int lane, Row row) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int k = min(32, n - i0);
-      const float lse = lane < k ? ld_dep(w.lse + row(i0 + lane)) : -INFINITY;
-      float top = lse;
+    constexpr int kBatch = 8;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float lse[kBatch];
+      uint4 raw[kBatch];
 #pragma unroll
-      for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const float m_new = fmaxf(m, top);
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      for (int i = 0; i < kBatch; ++i) {
+        lse[i] = -INFINITY;
+        if (i0 + i < n) {
+          const int64_t at = row(i0 + i);
+          lse[i] = ld_dep(w.lse + at);
+          raw[i] = ld_dep(reinterpret_cast<const uint4*>(w.o + at * kHeadDim) + lane);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, lse[i]);
+      const float ref = top == -INFINITY ? 0.f : top;
       const float f = fast_exp2(m - ref);
-      const float wt = fast_exp2(lse - ref);
+      m = top;
       den *= f;
       r.x *= f; r.y *= f; r.z *= f; r.w *= f;
-      m = m_new;
-#pragma unroll 4
-      for (int i = 0; i < k; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, wt, i);
-        const uint4 raw = ld_dep(reinterpret_cast<const uint4*>(w.o + row(i0 + i) * kHeadDim) + lane);
-        den += wi;
-        r.x = fmaf(wi, __uint_as_float(raw.x), r.x);
-        r.y = fmaf(wi, __uint_as_float(raw.y), r.y);
-        r.z = fmaf(wi, __uint_as_float(raw.z), r.z);
-        r.w = fmaf(wi, __uint_as_float(raw.w), r.w);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (i0 + i < n) {
+          const float wt = fast_exp2(lse[i] - ref);
+          den += wt;
+          r.x = fmaf(wt, __uint_as_float(raw[i].x), r.x);
+          r.y = fmaf(wt, __uint_as_float(raw[i].y), r.y);
+          r.z = fmaf(wt, __uint_as_float(raw[i].z), r.z);
+          r.w = fmaf(wt, __uint_as_float(raw[i].w), r.w);
+        }
       }
     }
   }
@@ -898,98 +1137,77 @@ struct Fold {
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Work work, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
-  if (!ld_dep(work.ok)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
-  const Partition part(*static_cast<const volatile int64_t*>(work.base), gridDim.x);
-  int64_t prev = -1;
+  const uint4 seg[2] = {ld_dep(reinterpret_cast<const uint4*>(work.seg + 2 * c)),
+                        ld_dep(reinterpret_cast<const uint4*>(work.seg + 2 * c + 1))};
+#pragma unroll
   for (int side = 0; side < 2; ++side) {
-    const uint4 a = ld_dep(reinterpret_cast<const uint4*>(work.seg + c * 4 + side * 2));
-    const uint4 b = ld_dep(reinterpret_cast<const uint4*>(work.seg + c * 4 + side * 2 + 1));
-    if (!b.z) continue;
-    const int64_t tile = static_cast<int64_t>(a.x) | (static_cast<int64_t>(a.y) << 32);
-    if (tile == prev) continue;
-    prev = tile;
-    const int lo = part.cta_of(tile), hi = part.cta_of(tile + a.z - 1);
-    if (lo == hi) continue;
-    const int n = hi - lo + 1, rows = kGroup * static_cast<int>(a.w);
-    const int lo_rec = 2 * lo + (part.start(lo) == tile ? 0 : 1);   // there it may come after other tiles
+    const uint4 a = seg[side];
+    if (!a.w) continue;
+    const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, rows = kGroup * static_cast<int>(a.y >> 8);
     for (int r = c - lo + n * warp; r < rows; r += n * kMergeWarps) {
       Fold f;
       f.add(work, n, lane, [&](int i) {
-        return static_cast<int64_t>(i == 0 ? lo_rec : 2 * (lo + i)) * work.rows_cap + r;
+        return static_cast<int64_t>(i == 0 ? static_cast<int>(a.w) - 1 : 2 * (lo + i)) * work.rows_cap + r;
       });
-      f.store(out, (static_cast<int64_t>(b.x) + (r >> 3)) * kNumQHeads + b.y * kGroup + (r & 7), lane);
+      f.store(out, (static_cast<int64_t>(a.x) + (r >> 3)) * kNumQHeads + (a.y & 0xff) * kGroup + (r & 7), lane);
     }
   }
 }
 
 // Prefix mode: a CTA per (sequence, KV head), a warp per query head: the
 // partials of its group's tile, then those of its own tokens.
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Plan plan, const Work work, int grid,
-                                                                     __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
-  if (!ld_dep(work.ok)) return;
   const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / kNumKVHeads, g = blockIdx.x % kNumKVHeads;
-  const int V = plan.groups + plan.B;
-  const volatile int64_t* base = work.base;
-  const Partition part(base[V], grid);
+  const int pair = blockIdx.x, pairs = B * kNumKVHeads;   // (sequence, KV head)
+  const int ok = ld_dep(work.ok);
+  int ends[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ends[i] = ld_dep(work.ends + i * static_cast<int64_t>(pairs) + pair);
+  if (!ok) return;
+  const int64_t row = static_cast<int64_t>(pair) * kGroup + h;   // query * 64 + head
   Fold f;
-  if (plan.groups > 0 && b < ld_dep(plan.cu + plan.groups)) {
-    int lo = 0, hi = plan.groups - 1;   // the group: the last one that starts at or before b and is not empty
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (ld_dep(plan.cu + mid) <= b) lo = mid; else hi = mid - 1;
-    }
-    const List s = load_list(plan, lo);
-    const int i = b - s.q0, t = i / kWideQ;
-    const int n = s.len > 0 ? (s.len + kChunkTokens - 1) / kChunkTokens : 1;
-    const int64_t first = base[lo] + (static_cast<int64_t>(g) * tiles_of(s) + t) * n;
-    const int c0 = part.cta_of(first), c1 = part.cta_of(first + n - 1);
-    const int64_t row = static_cast<int64_t>(kGroup) * (8ll * s.q0 + g * static_cast<int64_t>(s.nq) + i) + h;
-    f.add(work, c1 - c0 + 1, lane, [&](int x) { return row + static_cast<int64_t>(c0 + x) * work.rows_cap; });
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    const int first = ends[2 * part], last = ends[2 * part + 1];
+    if (first == kNone) continue;
+    const int c0 = first & 0xff;
+    const int64_t slots = 2ll * kNumQHeads * B + ((first >> kEndPlace) & 0xff) * kGroup + h;
+    const bool whole = first & kEndWhole;
+    f.add(work, whole ? 1 : last - c0 + 1, lane, [&](int i) {
+      return whole ? row + part * static_cast<int64_t>(kNumQHeads) * B
+                   : slots + (2ll * (c0 + i) + (i == 0 && (first & kEndSlot) ? 1 : 0)) * work.rows_cap;
+    });
   }
-  {
-    const List s = load_list(plan, plan.groups + b);
-    const int n = s.len > 0 ? (s.len + kChunkTokens - 1) / kChunkTokens : 1;
-    const int64_t first = base[plan.groups + b] + static_cast<int64_t>(g) * n;
-    const int c0 = part.cta_of(first), c1 = part.cta_of(first + n - 1);
-    const int64_t row = 64ll * plan.B + 64ll * b + kGroup * g + h;
-    f.add(work, c1 - c0 + 1, lane, [&](int x) { return row + static_cast<int64_t>(c0 + x) * work.rows_cap; });
-  }
-  f.store(out, static_cast<int64_t>(b) * kNumQHeads + g * kGroup + h, lane);
+  f.store(out, row, lane);
 }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-// The workspace's parts: records, their log-sum-exps, the first units of the
-// lists, the CTAs' segments, the verdict.
-size_t layout(Work* w, void* at, int64_t record_rows, int64_t lists, int rows_cap) {
-  const size_t o = static_cast<size_t>(record_rows) * kHeadDim * 4, lse = round16(record_rows * 4);
-  const size_t base = round16((lists + 1) * 8), seg = kMaxCtas * 4 * sizeof(int4), ok = 16;
+// Rows of a record: a tile's queries x 8 heads.
+int rows_cap(int queries) { return kGroup * (queries < kWideQ ? queries : kWideQ); }
+// The workspace's parts: rows and their log-sum-exps, the segments or the ends, the verdict.
+size_t layout(Work* w, void* at, int64_t place_rows, int queries, int64_t pairs) {
+  const int64_t rows = place_rows + 2ll * kMaxCtas * rows_cap(queries);
+  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4);
+  const size_t seg = 2 * kMaxCtas * sizeof(int4), ends = round16(4 * pairs * 4), ok = 16;
   if (w) {
     char* p = static_cast<char*>(at);
     w->o = reinterpret_cast<float*>(p);
     w->lse = reinterpret_cast<float*>(p += o);
-    w->base = reinterpret_cast<int64_t*>(p += lse);
-    w->seg = reinterpret_cast<int4*>(p += base);
-    w->ok = reinterpret_cast<int*>(p += seg);
-    w->rows_cap = rows_cap;
+    w->seg = reinterpret_cast<int4*>(p += lse);
+    w->ends = reinterpret_cast<int*>(p += seg);
+    w->ok = reinterpret_cast<int*>(p += ends);
+    w->rows_cap = rows_cap(queries);
   }
-  return o + lse + base + seg + ok;
+  return o + lse + seg + ends + ok;
 }
-// Rows of a record: a tile's queries x 8 heads.
-int rows_cap(int queries) { return kGroup * (queries < kWideQ ? queries : kWideQ); }
-size_t window_layout(Work* w, void* at, int max_q) {
-  return layout(w, at, 2ll * kMaxCtas * rows_cap(max_q), 0, rows_cap(max_q));   // first and last segment of each CTA
-}
-// Each row of the batch has a place for its prefix and one for its own tokens,
-// shifted by a record for each CTA, so that all partials of a tile fit in order.
-size_t prefix_layout(Work* w, void* at, int B, int groups) {
-  return layout(w, at, 2ll * kNumQHeads * B + static_cast<int64_t>(kMaxCtas) * rows_cap(B), groups + static_cast<int64_t>(B),
-                rows_cap(B));
+size_t window_layout(Work* w, void* at, int max_q) { return layout(w, at, 0, max_q, 0); }
+size_t prefix_layout(Work* w, void* at, int B) {
+  return layout(w, at, 2ll * kNumQHeads * B, B, static_cast<int64_t>(B) * kNumKVHeads);
 }
 
 std::mutex g_mu;
@@ -1059,7 +1277,7 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   launch_pdl(true, pool_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q, tm_q1, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (plan.prefix_mode)
-    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(kMergeThreads), 0, s, plan, work, grid, o);
+    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(kMergeThreads), 0, s, work, plan.B, o);
   else
     launch_pdl(true, window_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, s, work, o);
   return launch_status();
@@ -1108,7 +1326,7 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
 
 size_t lsa_prefix_attn_workspace_size(int B, int n_groups) {
   if (B <= 0 || B > LSA_MAX_BATCH || n_groups < 0 || n_groups > B) return 0;
-  return lsa::pool::prefix_layout(nullptr, nullptr, B, n_groups);
+  return lsa::pool::prefix_layout(nullptr, nullptr, B);
 }
 
 int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool, int64_t n_slots,
@@ -1122,7 +1340,7 @@ int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool
   const int st = pool::check(q, k_pool, v_pool, n_slots, suffix_len, B, max_chunks, softmax_scale, out);
   if (st != LSA_OK) return st;
   if (max_prefix_chunks > (1 << 23)) return LSA_ERR_UNSUPPORTED_SHAPE;
-  if (!workspace || workspace_bytes < pool::prefix_layout(nullptr, nullptr, B, n_groups)) return LSA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < pool::prefix_layout(nullptr, nullptr, B)) return LSA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LSA_ERR_MISALIGNED;
   pool::Plan plan = {};
   plan.prefix_mode = 1;
@@ -1138,7 +1356,7 @@ int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool
   plan.group_chunks = max_prefix_chunks;
   plan.n_slots = n_slots;
   pool::Work work;
-  pool::prefix_layout(&work, workspace, B, n_groups);
+  pool::prefix_layout(&work, workspace, B);
   const int64_t tiles = n_groups > 0 ? B / pool::kWideQ + n_groups : 0;
   const int64_t units = kNumKVHeads * (tiles * max_prefix_chunks + static_cast<int64_t>(B) * max_chunks);
   return pool::launch(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
