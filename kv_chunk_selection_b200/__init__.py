@@ -647,11 +647,12 @@ def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk
 
 
 def new_window_attn_workspace(B: int, max_q: int, device=None) -> torch.Tensor:
-    """A workspace for lsa_window_attn with up to ``max_q`` queries per sequence (it needs no initialisation)."""
+    """A workspace for lsa_window_attn with up to ``max_q`` queries per sequence, zeroed (every call leaves its
+    counts zero)."""
     n = int(_load().lsa_window_attn_workspace_size(int(B), int(max_q)))
     if n == 0:
         raise ValueError("unsupported batch")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
 def _pool_attn_args(q, k_pool, v_pool, chunk_table, lengths, max_chunks, out, workspace, name):
@@ -699,11 +700,11 @@ def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, m
 
 
 def new_prefix_attn_workspace(B: int, n_groups: int, device=None) -> torch.Tensor:
-    """A workspace for lsa_prefix_decode_attn (it needs no initialisation)."""
+    """A workspace for lsa_prefix_decode_attn, zeroed (every call leaves its counts zero)."""
     n = int(_load().lsa_prefix_attn_workspace_size(int(B), int(n_groups)))
     if n == 0:
         raise ValueError("unsupported batch")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
 def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len, chunk_table, suffix_len, out, workspace,

@@ -10,36 +10,44 @@
 //
 //   out = sum_j softmax_j(scale q . k_j) v_j
 //
-// One kernel serves both.  Its work is a list of units: a unit is 64 tokens
-// (one chunk) of K and V of one KV head, 32 KiB, against a tile of up to 32
-// queries (x 8 query heads = 256 rows).  The units of all tiles are laid end
-// to end and the grid (one CTA per SM) cuts the list into equal contiguous
-// ranges, so a single token over a long window and a long prompt both fill the
-// chip; a tile that a cut splits leaves one partial per CTA (normalised rows
-// and their log-sum-exps), which a second kernel folds in CTA order.
+// One kernel and one launch serve both.  The work is two lists of units; a unit
+// is 64 tokens (one chunk) of K and V of one KV head, 32 KiB, against the
+// queries of a tile:
+//   wide tiles    9 to 32 queries (x 8 query heads): prompts, large groups;
+//   narrow tiles  up to 8: single tokens, the tokens behind a shared prefix.
+// The units of a list's tiles are laid end to end (a tile's also count kTileCost
+// more, for its start and its end) and cut into equal contiguous shares: one
+// per CTA for the wide list, two per CTA for the narrow one.  So one token over
+// a long window, a ragged batch and a long prompt all fill the chip evenly.  A
+// tile that a cut splits leaves partials (normalised rows and their
+// log-sum-exps), which are folded in the order of the shares, so that the result
+// does not depend on timing: by the warp that adds a tile's last one where a
+// window call has narrow tiles only (no second launch), else by a second kernel
+// (the partials of wide tiles are too many for one SM: 32 sequences over a
+// prefix of 32768 tokens leave 19 MB).
 //
-// Roles of a CTA (12 warps):
-//   warps 0-3, 4-7  two softmax warpgroups, a thread per row: the scores of a
-//                   unit come from TMEM, the probabilities go back to TMEM in
-//                   the scores' place as bf16.  The running maximum is only
-//                   raised when it grows by more than 2^8 (the sums stay
-//                   exact, the accumulator is rescaled rarely);
-//   warps 8, 9      issue the tcgen05.mma of a warpgroup each: S = Q K^T (128 x
-//                   64 x 128), and O += P V (128 x 128 x 64) with P from TMEM;
-//   warp 10         streams the units with TMA into a ring of 4 stages;
-//   warp 11         walks the list, a few segments ahead of the others, and
-//                   loads the query tiles.
-// A tile of more than 16 queries is "wide": each warpgroup has 16 queries (128
-// rows) and both use every unit.  A smaller tile is "narrow": both warpgroups
-// have the same rows and take alternate units, so that the softmax of one unit
-// runs beside the products of the next, and their two accumulators are joined
-// at the end; that carries single tokens at the rate of the memory although 8
-// of 128 rows of a product are theirs.
+// A CTA (one per SM, 12 warps) has two pipelines w = 0, 1 of
+//   warps 4w..4w+3  a softmax warpgroup, a thread per row: the scores of a unit
+//                   come from TMEM, the probabilities go back in their place as
+//                   bf16.  The running maximum is only raised when it grows by
+//                   more than 2^8 (the sums stay exact, the accumulator is
+//                   rescaled rarely);
+//   warp 8 + w      issues the tcgen05.mma: S = Q K^T (128 x 64 x 128) into one
+//                   of two score buffers, O += P V (128 x 128 x 64) with P from
+//                   TMEM;
+//   warp 10 + w     plans and loads (TMA).
+// First the CTA's wide share: both pipelines use every unit, each with half of
+// the tile's queries; warp 10 streams K and V through all 8 half-stages of 16
+// KiB, warp 11 walks the list a few segments ahead and loads the queries.  Then
+// the narrow shares: each pipeline has its own stream through 4 half-stages, so
+// that one's start of a tile, its latencies and its end run beside the other's
+// units; that carries single tokens at the rate of the memory although 8 of the
+// 128 rows of a product are theirs.
 //
-// TMEM (512 columns): scores 2 warpgroups x 2 buffers x 64, accumulators 2 x
-// 128.  Rows that no query of a tile sees are zeroed in V's stage before the
-// product, so a page's unwritten tail may hold anything (0 times NaN is NaN);
-// the scores there are masked by selection.
+// TMEM (512 columns): scores 2 pipelines x 2 buffers x 64, accumulators 2 x 128.
+// Rows that no query of a tile sees are zeroed in V's stage before the product,
+// so a page's unwritten tail may hold anything (0 times NaN is NaN); the scores
+// there are masked by selection.
 #include <math.h>
 
 #include <mutex>
@@ -50,30 +58,31 @@
 namespace lsa {
 namespace pool {
 
-constexpr int kWideQ = 32;                   // queries of a tile
-constexpr int kHalfQ = 16;                   // queries of a warpgroup: 16 x 8 heads = 128 rows
-constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8;                  // and 9: one for each softmax warpgroup
-constexpr int kLoadWarp = 10, kPlanWarp = 11;
+constexpr int kWideQ = 32, kNarrowQ = 8;     // queries of a wide tile, of a narrow one
+constexpr int kMmaWarp = 8, kLoadWarp = 10;  // of pipeline 0; 9 and 11 are pipeline 1's
 constexpr int kThreads = 12 * 32;
-constexpr int kStages = 4;
+constexpr int kHalves = 8;                   // half-stages: a unit's K or V of one head
 constexpr int kBoxBytes = 8192;              // 64 tokens x 64 dims
-constexpr int kStageBytes = 4 * kBoxBytes;   // K dims 0-63, 64-127, V dims 0-63, 64-127
+constexpr int kHalfBytes = 2 * kBoxBytes;
 constexpr int kQBoxBytes = 16384;            // 128 rows x 64 dims
 constexpr int kQTileBytes = 2 * kQBoxBytes;
+constexpr int kQ2Bytes = 8192;               // a pipeline's second narrow query tile: rows 64.. of its region
 constexpr int kTurnBytes = 4096;             // a warp's rows on their way out: 32 rows x 128 bytes
-constexpr int kAhead = 8;                    // places for segments that the planner is ahead
+constexpr int kAhead = 4;                    // places for segments that a planner is ahead
 constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
-#ifndef FMA_EVERY
-#define FMA_EVERY 4
+#ifndef TILE_COST
+#define TILE_COST 3
 #endif
-constexpr int kFmaEvery = FMA_EVERY;
+constexpr int kTileCost = TILE_COST;
+#ifndef MIN_SHARE
+#define MIN_SHARE 6
+#endif
+constexpr int kMinShare = MIN_SHARE;         // smallest share of a list worth a pipeline (or a CTA) of its own
+constexpr int kFmaEvery = 4;                 // of the pairs of powers of two, one in 4 on the FMA pipe
 constexpr float kRaise = 8.f;                // growth of the maximum (log2) that rescales the accumulator
 constexpr int kSCols = 64, kOCol0 = 256;     // TMEM: S[w][b] at (2 w + b) * 64, O[w] at 256 + 128 w
-constexpr int64_t kMinUnitsPerCta = 2;
 
 struct Plan {
-  int prefix_mode;
   int B, groups;             // groups: prefix mode only
   int64_t rows;              // queries in q
   const int32_t* cu;         // cu_q [B + 1], or cu_group [groups + 1]
@@ -84,39 +93,53 @@ struct Plan {
   int max_chunks, group_chunks;
   int max_q, window, sinks;
   int64_t n_slots;
-  __device__ int lists() const { return prefix_mode ? groups + B : B; }
 };
+// What a launch can meet: a window call whose sequences have at most kNarrowQ
+// queries (narrow tiles only, folded in the kernel), any window call, a prefix
+// call.  Each has only its own code: the softmax loop has no registers to spare.
+enum Mode { kWindowNarrow, kWindow, kPrefixes };
 
-// Partials.  A CTA's first and last segment can be part of a tile: they have a
-// record each, slots 2c and 2c + 1, of rows_cap rows (query x head).  In window
-// mode a whole tile goes straight to the output; in prefix mode its rows have
-// places of their own, 64 per sequence for its prefix and 64 for its own tokens,
-// after which the slots follow.
+// Partials.  The first and the last segment of a share can be part of a tile:
+// share c has two records, slots 2c and 2c + 1, of as many rows as its kind of
+// tile has.  In prefix mode the rows of a whole tile have places of their own,
+// 64 per sequence for its prefix and 64 for its own tokens, since a sequence's
+// output joins both.
 struct Work {
-  float* o;          // [rows][128], normalised
+  float* o;          // [rows][128], normalised: the places, the wide slots, the narrow slots
   float* lse;        // [rows], base 2
-  int4* seg;         // window mode: [2 * kMaxCtas], a slot's tile: first query, KV head and queries,
-                     // first and last CTA, slot of the first CTA's record + 1 (0: nothing to fold)
+  int64_t slots[2];  // first row of the narrow slots, of the wide ones
+  int rows[2];       // rows of a narrow record, of a wide one
+  int* count;        // kWindowNarrow: [2 kMaxCtas][2 warps], by a tile's first share: units that
+                     // its partials hold so far, zero between calls
+  int4* parts;       // kWindow: by slot (wide, then narrow), its tile: first query, KV head and
+                     // queries, first and last share, slot of the first share's partial + 1 (0: none)
   int* ends;         // prefix mode: [4][8 B], by (sequence, KV head): first and last partial of the
                      // prefix, of the own tokens
   int* ok;           // prefix mode: the offsets were valid
-  int rows_cap;
 };
-// The first partial of a (sequence, KV head): CTA, slot 2c + bit, the query's
-// place in the tile, or that the rows are in their own place; kNone: no partial.
-constexpr int kEndSlot = 1 << 8, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
+// The first partial of a (sequence, KV head): its share, slot 2c + bit, whether
+// of the wide list, the query's place in the tile, or that the rows are in
+// their own place; kNone: no partial.
+constexpr int kEndShare = 0x3ff, kEndSlot = 1 << 10, kEndWide = 1 << 11, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
 
-// The queries and the keys of one list: a sequence, or a group over its prefix.
+// The queries and the keys of one list entry: a sequence, or a group over its prefix.
 struct List {
   int q0, nq, len;
   const int32_t* table;
   int64_t ident;             // identity layout: slot of chunk 0 (table null)
 };
 
+__device__ __forceinline__ int chunks_of(int len) { return len > 0 ? (len + kChunkTokens - 1) / kChunkTokens : 0; }
+// A length out of range counts as none (-1; the scan reports it).
+__device__ __forceinline__ int checked_len(int len, int chunks) {
+  return len < 0 || len > chunks * kChunkTokens ? -1 : len;
+}
+
+template <bool kPrefix>
 __device__ __forceinline__ List load_list(const Plan& p, int v) {
   List s;
   int cap;
-  if (p.prefix_mode && v >= p.groups) {
+  if (kPrefix && v >= p.groups) {
     const int b = v - p.groups;
     s.q0 = b;
     s.nq = 1;
@@ -127,17 +150,22 @@ __device__ __forceinline__ List load_list(const Plan& p, int v) {
   } else {
     s.q0 = ld_dep(p.cu + v);
     s.nq = ld_dep(p.cu + v + 1) - s.q0;
-    s.len = ld_dep((p.prefix_mode ? p.group_len : p.len) + v);
-    cap = p.prefix_mode ? p.group_chunks : p.max_chunks;
+    s.len = ld_dep((kPrefix ? p.group_len : p.len) + v);
+    cap = kPrefix ? p.group_chunks : p.max_chunks;
     s.ident = static_cast<int64_t>(v) * cap;
-    const int32_t* t = p.prefix_mode ? p.group_table : p.table;
+    const int32_t* t = kPrefix ? p.group_table : p.table;
     s.table = t ? t + s.ident : nullptr;
   }
-  if (s.len < 0 || s.len > cap * kChunkTokens) s.len = -1;   // reported by the scan
+  s.len = checked_len(s.len, cap);
   return s;
 }
 
-__device__ __forceinline__ int tiles_of(const List& s) { return (s.nq + kWideQ - 1) / kWideQ; }
+// Tiles are 32 queries long; the last one of an entry is narrow when it has at
+// most 8.
+__device__ __forceinline__ int tiles_of(const List& s, bool wide) {
+  const int rest = s.nq % kWideQ;
+  return wide ? s.nq / kWideQ + (rest > kNarrowQ) : (rest > 0 && rest <= kNarrowQ);
+}
 
 // sum over y < x of floor(y / 2)
 __device__ __forceinline__ int64_t half_sum(int64_t x) { return x > 0 ? (x - 1) * (x - 1) / 4 : 0; }
@@ -151,87 +179,117 @@ __device__ __forceinline__ int64_t chunk_sum(int a, int t, int64_t cap) {
   return half_sum(b1) - half_sum(b0) + cap * ((x1 - b1) - (x0 - b0));
 }
 
-// Units of the first t tiles of a list, for one KV head.  A tile without a key
-// in sight still has one (empty) unit, so that its rows are written.
-__device__ __forceinline__ int64_t units_before(const Plan& p, const List& s, int t) {
-  if (p.prefix_mode) {
-    const int n = s.len > 0 ? (s.len + kChunkTokens - 1) / kChunkTokens : 1;
-    return static_cast<int64_t>(t) * n;
+// Window mode, a tile of `cnt` queries from position p0 on: the first chunk of
+// its window and the sink chunks before it; returns the chunks that it sees.
+__device__ __forceinline__ int tile_chunks(const Plan& p, int p0, int cnt, int& low, int& first) {
+  const int p1 = p0 + cnt - 1;
+  low = max(0, p0 - p.window + 1) >> 6;
+  first = min(low, (p.sinks + kChunkTokens - 1) / kChunkTokens);
+  return p1 < 0 ? 0 : (p1 >> 6) - low + 1 + first;
+}
+
+// Units, with kTileCost for each tile, of the first t wide tiles of an entry, or
+// of its narrow tile (t = 1), for one KV head.  A tile without a key in sight
+// still has one (empty) unit, so that its rows are written.
+template <bool kPrefix>
+__device__ __forceinline__ int64_t span(const Plan& p, const List& s, bool wide, int t) {
+  if (t <= 0) return 0;
+  if (kPrefix) return static_cast<int64_t>(t) * (max(1, chunks_of(s.len)) + kTileCost);
+  const int pos0 = max(s.len, 0) - s.nq;
+  if (!wide) {
+    int low, first;
+    const int rest = s.nq % kWideQ;
+    return max(1, tile_chunks(p, pos0 + s.nq - rest, rest, low, first)) + kTileCost;
   }
-  const int pos0 = (s.len < 0 ? 0 : s.len) - s.nq;
   const int64_t none = int64_t{1} << 40;
   const int a_low = pos0 - p.window + 1;
-  int64_t n = chunk_sum(pos0 + kWideQ - 1, t, none) + t - chunk_sum(a_low, t, none) +
-              chunk_sum(a_low, t, (p.sinks + kChunkTokens - 1) / kChunkTokens);
-  if (t > 0 && t * kWideQ > s.nq) {   // the last tile ends before its 32nd query
+  int64_t n = chunk_sum(pos0 + kWideQ - 1, t, none) - chunk_sum(a_low, t, none) +
+              chunk_sum(a_low, t, (p.sinks + kChunkTokens - 1) / kChunkTokens) + static_cast<int64_t>(t) * (1 + kTileCost);
+  if (t * kWideQ > s.nq) {   // the last tile ends before its 32nd query
     const int full = (pos0 + t * kWideQ - 1) >> 6, real = (pos0 + s.nq - 1) >> 6;
     n += (real > 0 ? real : 0) - (full > 0 ? full : 0);
   }
   return n;
+}
+template <bool kPrefix>
+__device__ __forceinline__ int64_t span(const Plan& p, const List& s, bool wide) {
+  return s.nq > 0 ? kNumKVHeads * span<kPrefix>(p, s, wide, tiles_of(s, wide)) : 0;
 }
 
 // A 64-bit quotient, in 32 bits where the operands allow it (five times faster).
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
+// A list cut into equal shares: at most `most`, none smaller than kMinShare
+// (unless it is the only one).
 struct Partition {
   int64_t base, rem;
-  __device__ Partition(int64_t total, int G) : base(quotient(total, G)), rem(total - base * G) {}
-  __device__ int64_t start(int c) const { return c * base + (c < rem ? c : rem); }
-  __device__ int cta_of(int64_t u) const {
+  int parts;
+  __device__ Partition(int64_t total, int most) {
+    const int64_t worth = quotient(total, kMinShare);
+    parts = static_cast<int>(worth < 1 ? 1 : worth < most ? worth : most);
+    base = quotient(total, parts);
+    rem = total - base * parts;
+  }
+  __device__ int64_t start(int c) const {
+    c = min(c, parts);
+    return c * base + (c < rem ? c : rem);
+  }
+  __device__ int share_of(int64_t u) const {
     const int64_t big = rem * (base + 1);
     return static_cast<int>(u < big ? quotient(u, base + 1) : rem + quotient(u - big, base));
   }
 };
 
-// A walk over the tiles of the unit list.
+// A walk over the tiles of one list, within a share [.., end).
+template <bool kPrefix>
 struct Cursor {
-  int v, g, t, j;            // list, KV head, tile, unit of the tile
+  int v, g, t, j;            // entry, KV head, tile, unit of the tile
   List s;
   int tiles;
-  int cnt;                   // queries of the tile
-  int n;                     // its units
+  int cnt, n;                // queries of the tile, its units
   int p0;                    // window mode: position of its first query
   int low, first;            // window mode: first chunk of the window, sink chunks before it
   bool empty;                // no key in sight: the one unit is empty
+  int64_t at, end;           // the tile's place in the list, the share's end
 
-  __device__ void set_tile(const Plan& p) {
-    cnt = min(kWideQ, s.nq - t * kWideQ);
-    if (p.prefix_mode) {
-      n = s.len > 0 ? (s.len + kChunkTokens - 1) / kChunkTokens : 0;
-      p0 = low = first = 0;
+  __device__ void set_tile(const Plan& p, bool wide) {
+    const int i = wide ? t * kWideQ : s.nq - s.nq % kWideQ;
+    cnt = min(kWideQ, s.nq - i);
+    p0 = low = first = 0;
+    if (kPrefix) {
+      n = chunks_of(s.len);
     } else {
-      p0 = (s.len < 0 ? 0 : s.len) - s.nq + t * kWideQ;
-      const int p1 = p0 + cnt - 1;
-      low = max(0, p0 - p.window + 1) >> 6;
-      first = min(low, (p.sinks + kChunkTokens - 1) / kChunkTokens);
-      n = p1 < 0 ? 0 : (p1 >> 6) - low + 1 + first;
+      p0 = max(s.len, 0) - s.nq + i;
+      n = tile_chunks(p, p0, cnt, low, first);
     }
     empty = n == 0;
     n = max(n, 1);
   }
-  __device__ void set_list(const Plan& p) {
-    s = load_list(p, v);
-    tiles = tiles_of(s);
-  }
-  // At unit r of list `list`, whose KV heads have per_head units each.
-  __device__ void start(const Plan& p, int list, const List& l, int64_t per_head, int64_t r) {
-    v = list;
+  __device__ int row(bool wide) const { return s.q0 + (wide ? t * kWideQ : s.nq - s.nq % kWideQ); }
+  // At place r of entry `entry`, whose KV heads have per_head places each; the
+  // place in the list is u.
+  __device__ void start(const Plan& p, bool wide, int entry, const List& l, int64_t per_head, int64_t r, int64_t u) {
+    v = entry;
     s = l;
-    tiles = tiles_of(s);
+    tiles = tiles_of(s, wide);
     g = static_cast<int>(quotient(r, per_head));
     r -= g * per_head;
     int lo = 0, hi = tiles - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (units_before(p, s, mid) <= r) lo = mid; else hi = mid - 1;
+      if (span<kPrefix>(p, s, wide, mid) <= r) lo = mid; else hi = mid - 1;
     }
     t = lo;
-    j = static_cast<int>(r - units_before(p, s, t));
-    set_tile(p);
+    r -= span<kPrefix>(p, s, wide, t);
+    at = u - r;
+    j = max(0, static_cast<int>(r) - kTileCost);
+    set_tile(p, wide);
   }
-  // To the first unit of the next tile; the caller knows that there is one.
-  __device__ void next(const Plan& p) {
+  // To the first unit of the next tile, if the share has any of it.
+  __device__ bool next(const Plan& p, bool wide) {
+    at += n + kTileCost;
+    if (at >= end) return false;
     j = 0;
     if (++t == tiles) {
       t = 0;
@@ -239,14 +297,19 @@ struct Cursor {
         g = 0;
         do {
           ++v;
-          set_list(p);
+          s = load_list<kPrefix>(p, v);
+          tiles = tiles_of(s, wide);
         } while (tiles == 0);
       }
     }
-    set_tile(p);
+    set_tile(p, wide);
+    return units() > 0;
   }
-  __device__ int chunk(int u) const { return u < first ? u : low + u - first; }
-  __device__ bool wide() const { return cnt > kHalfQ; }
+  // Units from j on that the share has.
+  __device__ int units() const {
+    const int64_t x = end - at - kTileCost;
+    return static_cast<int>(x < n ? x : n) - j;
+  }
 };
 
 // 64 bits: the lowest x.
@@ -484,42 +547,163 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sm, int64_t* t
   return before + inc - x;
 }
 
-// A segment: the units of one tile that this CTA has.  The planner warp writes
-// them to shared memory a few ahead, so that no other role walks the list or
-// waits for its loads.
+// ---- folding the partials -----------------------------------------------------
+__device__ __forceinline__ uint4 ld_l2(const float4* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_l2(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+// The kRows rows from a first one on, of the n partials whose first rows are
+// row(0) .. row(n - 1): joins them in that order and writes bf16 to out.  A warp,
+// 4 dims a lane; the loads of 32 / kRows partials are in flight together.
+template <int kRows, typename Row>
+__device__ __forceinline__ void fold_rows(const Work& w, int n, int lane, Row row, __nv_bfloat16* out) {
+  constexpr int kBatch = kRows >= 8 ? 2 : 16 / kRows;
+  float m[kRows], den[kRows];
+  float4 acc[kRows];
+#pragma unroll
+  for (int h = 0; h < kRows; ++h) {
+    m[h] = -INFINITY;
+    den[h] = 0.f;
+    acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 1
+  for (int i = 0; i < n; i += kBatch) {
+    float lse[kBatch][kRows];
+    uint4 a[kBatch][kRows];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+#pragma unroll
+      for (int h = 0; h < kRows; ++h) {
+        lse[x][h] = -INFINITY;
+        a[x][h] = make_uint4(0, 0, 0, 0);
+      }
+      if (i + x < n) {
+        const int64_t r = row(i + x);
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+          lse[x][h] = ld_l2(w.lse + r + h);
+          a[x][h] = ld_l2(reinterpret_cast<const float4*>(w.o + (r + h) * kHeadDim) + lane);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kRows; ++h) {
+      float top = m[h];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) top = max3(top, lse[x][h], lse[x][h]);   // (a row that is not a number stays so)
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float f = fast_exp2(m[h] - ref);
+      m[h] = top;
+      den[h] *= f;
+      acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const float wt = fast_exp2(lse[x][h] - ref);
+        den[h] += wt;
+        acc[h].x = fmaf(wt, __uint_as_float(a[x][h].x), acc[h].x);
+        acc[h].y = fmaf(wt, __uint_as_float(a[x][h].y), acc[h].y);
+        acc[h].z = fmaf(wt, __uint_as_float(a[x][h].z), acc[h].z);
+        acc[h].w = fmaf(wt, __uint_as_float(a[x][h].w), acc[h].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kRows; ++h) {
+    const float id = den[h] == 0.f ? 0.f : 1.f / den[h];
+    *reinterpret_cast<uint2*>(out + h * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16(acc[h].x * id, acc[h].y * id), pack_bf16(acc[h].z * id, acc[h].w * id));
+  }
+}
+template <typename Row>
+__device__ __forceinline__ void fold_query(const Work& w, int n, int lane, Row row, __nv_bfloat16* out) {
+  if (n <= 2) {
+    fold_rows<kGroup>(w, n, lane, row, out);
+  } else {
+#pragma unroll 1
+    for (int h = 0; h < kGroup; h += 4)
+      fold_rows<4>(w, n, lane, [&](int i) -> int64_t { return row(i) + h; }, out + h * kHeadDim);
+  }
+}
+
+// A segment: the units of one tile that a share has.  The planners write them to
+// shared memory a few ahead, so that no other role walks the list or waits for
+// its loads.
 struct Seg {
-  int units;                 // 0: the list has ended
-  int flags;                 // kSegWide ...
+  int units;                 // 0: the share has ended
+  int flags;                 // kSegEmpty ...
   int j0;                    // its first unit in the tile
   int cnt, row, head;        // the tile's queries, the first one's row of q, the first query head
   int first, low;            // chunk of unit j: j < first ? j : low + j - first
   int f0, f1, f2;            // units that every query sees whole: j < f0 and f1 <= j <= f2
   int p0, len;               // window mode: position of the first query; prefix mode: tokens
+  int share, index;          // the share, the segment's index in it
+  int lo, hi;                // window mode: first and last share of the tile
+  int slot0;                 // window mode: the slot of the first share's partial
+  int all;                   // units of the tile
   int g;
   const int32_t* table;
   int64_t ident;
 };
-constexpr int kSegWide = 1, kSegEmpty = 2, kSegAgain = 4, kSegGroup = 8, kSegWhole = 16;
+constexpr int kSegEmpty = 1, kSegAgain = 2, kSegGroup = 4, kSegWhole = 8, kSegAlone = 16;
 
 // Shared memory, from a 1024-byte boundary.
-constexpr int kQAt = kStages * kStageBytes, kTurnAt = kQAt + 2 * kQTileBytes, kMlAt = kTurnAt + 8 * kTurnBytes;
-constexpr int kSegAt = kMlAt + 2 * 2 * 128 * 4, kBarAt = kSegAt + kAhead * static_cast<int>(sizeof(Seg));
+constexpr int kQAt = kHalves * kHalfBytes, kTurnAt = kQAt + 2 * kQTileBytes;
+constexpr int kSegAt = kTurnAt + 8 * kTurnBytes;   // [3][kAhead]: the wide share's, each pipeline's narrow share's
 // Barriers, 8 bytes each.
-constexpr int kFull = kBarAt, kEmpty = kFull + 8 * kStages;            // ring stages
-constexpr int kSFull = kEmpty + 8 * kStages;                            // [2 warpgroups][2 buffers] scores are there
-constexpr int kPFull = kSFull + 32, kODone = kPFull + 32;               // probabilities are; the product that read them is done
-constexpr int kQFull = kODone + 32, kQEmpty = kQFull + 8;
-constexpr int kSegFull = kQEmpty + 8, kSegEmptied = kSegFull + 8 * kAhead;
-constexpr int kMeet = kSegEmptied + 8 * kAhead, kReady = kMeet + 8;     // both warpgroups; the scratch has been read
-constexpr int kDrain = kReady + 8;                                      // [2]
+constexpr int kBarAt = kSegAt + 3 * kAhead * static_cast<int>(sizeof(Seg));
+constexpr int kFull = kBarAt, kEmpty = kFull + 8 * kHalves;            // half-stages
+constexpr int kSFull = kEmpty + 8 * kHalves;                           // [2 pipelines][2 buffers] scores are there
+constexpr int kPFull = kSFull + 32, kODone = kPFull + 32;              // probabilities are; the product that read them is done
+constexpr int kQFull = kODone + 32, kQEmpty = kQFull + 16;             // [2] query tiles of the wide share
+constexpr int kNFull = kQEmpty + 16, kNEmpty = kNFull + 32;            // [2 pipelines][2] of the narrow ones
+constexpr int kSegFull = kNEmpty + 32, kSegDone = kSegFull + 24 * kAhead;   // [3][kAhead]
+constexpr int kHandOver = kSegDone + 24 * kAhead;                      // [2]: 11's part of the wide share is done, 10's is
+constexpr int kDrain = kHandOver + 16;                                 // [2]
 constexpr int kTmemAt = kDrain + 16, kAbortAt = kTmemAt + 4;
-constexpr int kSmemBytes = kAbortAt + 4;
-static_assert(kSmemBytes <= 232448 && sizeof(Seg) % 8 == 0, "shared memory of one CTA");
+// The entry at the start of the wide share and of the two narrow ones.
+struct Found {
+  List s;
+  int64_t r, per_head;       // the place in the entry, the entry's places per KV head
+  int v;
+};
+constexpr int kFoundAt = kAbortAt + 4;
+constexpr int kSmemBytes = kFoundAt + 3 * static_cast<int>(sizeof(Found));
+static_assert(kSmemBytes <= 232448 && sizeof(Seg) % 8 == 0 && kFoundAt % 8 == 0, "shared memory of one CTA");
 
+// The place in the ring of the x-th half (K of unit i: 2 i, V: 2 i + 1) of a
+// share, and the parity of its use.  The wide share goes around all 8; the
+// narrow one of pipeline w around 4w .. 4w + 3, with the wide share's uses before
+// (`base`: their parity, `used`: whether there were any, a bit per half).
+struct Ring {
+  unsigned first, mask, shift, base, used;
+  __device__ unsigned half(unsigned x) const { return first + (x & mask); }
+  __device__ unsigned parity(unsigned x) const { return ((x >> shift) ^ (base >> half(x))) & 1; }
+};
+__device__ __forceinline__ Ring wide_ring() { return {0, 7, 3, 0, 0}; }
+__device__ __forceinline__ Ring narrow_ring(int w, unsigned wide_units) {
+  unsigned base = 0, used = 0;
+  for (unsigned h = 0; h < kHalves; ++h) {
+    const unsigned uses = (2 * wide_units + 7 - h) >> 3;
+    base |= (uses & 1) << h;
+    used |= (uses ? 1u : 0u) << h;
+  }
+  return {4u * w, 3, 2, base, used};
+}
+
+template <Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1, const Plan plan,
-                 const Work work, float scale_log2, __nv_bfloat16* __restrict__ out, unsigned* status) {
+                 const __grid_constant__ CUtensorMap tm_q16, const __grid_constant__ CUtensorMap tm_q8,
+                 const __grid_constant__ CUtensorMap tm_q1, const Plan plan, const Work work, float scale_log2,
+                 __nv_bfloat16* __restrict__ out, unsigned* status) {
+  constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowNarrow, kHasWide = kMode != kWindowNarrow;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sm = smem_u32(smem);
@@ -527,7 +711,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
   // ---- before the previous kernel has ended: barriers and TMEM ---------------
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kHalves; ++i) {
       bar_init(sm + kFull + 8 * i, 1);
       bar_init(sm + kEmpty + 8 * i, 2);   // both product warps (or one of them twice)
     }
@@ -535,17 +719,19 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       bar_init(sm + kSFull + 8 * i, 1);
       bar_init(sm + kPFull + 8 * i, 4);   // the warps of the warpgroup
       bar_init(sm + kODone + 8 * i, 1);
+      bar_init(sm + kNFull + 8 * i, 1);
+      bar_init(sm + kNEmpty + 8 * i, 1);
     }
-    bar_init(sm + kQFull, 1);
-    bar_init(sm + kQEmpty, 2);
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(sm + kQFull + 8 * i, 1);
+      bar_init(sm + kQEmpty + 8 * i, 1);
+      bar_init(sm + kHandOver + 8 * i, 1);
+      bar_init(sm + kDrain + 8 * i, 1);
+    }
+    for (int i = 0; i < 3 * kAhead; ++i) {
       bar_init(sm + kSegFull + 8 * i, 1);
-      bar_init(sm + kSegEmptied + 8 * i, 11);   // softmax, product and load warps
+      bar_init(sm + kSegDone + 8 * i, i < kAhead ? 11 : 5);   // softmax, product and (wide) load warps
     }
-    bar_init(sm + kMeet, kSoftmaxThreads / 32);
-    bar_init(sm + kReady, 1);
-    bar_init(sm + kDrain, 1);
-    bar_init(sm + kDrain + 8, 1);
     *reinterpret_cast<volatile int*>(smem + kAbortAt) = 0;
     mbar_fence_init();
   }
@@ -553,124 +739,136 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   if (tid == kLoadWarp * 32) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_q16);
+    tma_prefetch_desc(&tm_q8);
     tma_prefetch_desc(&tm_q1);
   }
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- the unit list: validity, total, and the place where this CTA starts --
-  // (The scratch lies in the ring, which is empty until the roles start.)
-  int64_t* scan = reinterpret_cast<int64_t*>(smem);
-  List* found = reinterpret_cast<List*>(scan + 40);
-  const int V = plan.lists();
+  // ---- the lists: validity, totals, and the places where the shares start ----
+  // (The scan's scratch lies where rows turn later.)
+  int64_t* const scan = reinterpret_cast<int64_t*>(smem + kTurnAt);
+  Found* const found = reinterpret_cast<Found*>(smem + kFoundAt);
+  const int V = plan.B + (kPrefix ? plan.groups : 0);
   const int per = (V + kThreads - 1) / kThreads;
   const int v_lo = min(V, tid * per), v_hi = min(V, v_lo + per);
   int bad = 0;
-  int64_t mine = 0;
-  const int n_cu = plan.prefix_mode ? plan.groups : plan.B;
+  int64_t mine[2] = {0, 0};   // [narrow, wide]
+  const int n_cu = kPrefix ? plan.groups : plan.B;
   if (tid == kThreads - 1 && n_cu > 0) {
-    bad |= ld_dep(plan.cu) != 0;
     const int last = ld_dep(plan.cu + n_cu);
-    bad |= last < 0 || last > plan.rows;
+    bad |= ld_dep(plan.cu) != 0 || last < 0 || last > plan.rows;
   }
-  auto units_of_list = [&](const List& s) {
-    return s.nq > 0 ? kNumKVHeads * units_before(plan, s, tiles_of(s)) : 0;
-  };
-  List s_last = {};   // the thread's last list: its only one for up to kThreads lists
+  List s_last = {};   // the thread's last entry: its only one for up to kThreads entries
   for (int v = v_lo; v < v_hi; ++v) {
-    s_last = load_list(plan, v);
+    s_last = load_list<kPrefix>(plan, v);
     if (s_last.len < 0 && blockIdx.x == 0) set_status(status, LSA_DEV_ERR_BAD_COUNT);
-    bad |= s_last.nq < 0 || (!plan.prefix_mode && s_last.nq > plan.max_q);
-    mine += units_of_list(s_last);
+    bad |= s_last.nq < 0 || s_last.nq > plan.max_q;
+    mine[0] += span<kPrefix>(plan, s_last, false);
+    if (kHasWide) mine[1] += span<kPrefix>(plan, s_last, true);
   }
-  int64_t total;
   bad = __syncthreads_or(bad);
-  const int64_t before = block_scan<kThreads / 32>(bad ? 0 : mine, scan, &total);
-  const Partition part(total, gridDim.x);
-  const int64_t u0 = part.start(blockIdx.x), u1 = part.start(blockIdx.x + 1);
-  if (part.base >= (1 << 30)) bad = 1;   // a CTA counts its units in 32 bits
+  if (bad) mine[0] = mine[1] = 0;
+  int64_t total[2];
+  int64_t before[2] = {block_scan<kThreads / 32>(mine[0], scan, &total[0]), 0};
+  total[1] = 0;
+  if (kHasWide) before[1] = block_scan<kThreads / 32>(mine[1], scan + 16, &total[1]);
+  const Partition part_n(total[0], 2 * gridDim.x), part_w(total[1], gridDim.x);
+  if (part_n.base >= (1 << 30) || part_w.base >= (1 << 30)) bad = 1;   // a share counts its units in 32 bits
   if (sm & 1023u) {                      // the 128-byte swizzle repeats every 1024 bytes
     if (tid == 0) set_status(status, LSA_DEV_ERR_INTERNAL);
     bad = 1;
   }
-  if (blockIdx.x == 0) {
-    if (tid == 0) {
-      if (bad) set_status(status, LSA_DEV_ERR_CAPACITY);
-      if (plan.prefix_mode) *work.ok = bad ? 0 : 1;
-    }
-    if (plan.prefix_mode && !bad)   // sequences behind the last group have no prefix
-      for (int x = (n_cu ? ld_dep(plan.cu + n_cu) : 0) * kNumKVHeads + tid; x < plan.B * kNumKVHeads; x += kThreads)
-        work.ends[x] = kNone;
-  }
-  const bool idle = bad || u0 >= u1;
-  if (!idle && before <= u0 && u0 < before + mine) {   // one thread: the list of unit u0
-    int64_t at = before, n = mine;
-    int v = v_lo;
-    if (per > 1) {
-      for (;; ++v) {
-        s_last = load_list(plan, v);
-        n = units_of_list(s_last);
-        if (u0 < at + n) break;
-        at += n;
+  if (bad && blockIdx.x == 0 && tid == 0) set_status(status, LSA_DEV_ERR_CAPACITY);
+  const int me = blockIdx.x;
+  // Prefix mode: sequences from `grouped` on belong to no group.
+  const int grouped = plan.groups ? ld_dep(plan.cu + plan.groups) : 0;
+  if (kPrefix && me == 0 && tid == 0) *work.ok = bad ? 0 : 1;
+#pragma unroll
+  for (int x = kHasWide ? 0 : 1; x < 3; ++x) {   // the entries at the starts of the wide share and of the two narrow ones
+    const int k = x == 0;
+    const int64_t u = x == 0 ? part_w.start(me) : part_n.start(2 * me + x - 1);
+    if (!bad && before[k] <= u && u < before[k] + mine[k]) {   // one thread, if u is in the list
+      int64_t at = before[k], n = mine[k];
+      int v = v_lo;
+      List s = s_last;
+      if (per > 1) {
+        for (;; ++v) {
+          s = load_list<kPrefix>(plan, v);
+          n = span<kPrefix>(plan, s, k);
+          if (u < at + n) break;
+          at += n;
+        }
       }
+      found[x] = {s, u - at, n / kNumKVHeads, v};
     }
-    *found = s_last;
-    scan[32] = v;
-    scan[33] = u0 - at;
-    scan[34] = n / kNumKVHeads;
   }
-  fence_proxy_async_smem();   // the scratch was written here; TMA writes it next
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = *reinterpret_cast<const volatile uint32_t*>(smem + kTmemAt);
   const Seg* const segs = reinterpret_cast<const Seg*>(smem + kSegAt);
   auto wait = [&](int bar, unsigned parity) { return bar_wait(sm + bar, parity, abort_flag, status); };
-  // Segment k of this CTA; its place is free again once every role has said so.
-  auto seg_get = [&](unsigned k) { return wait(kSegFull + 8 * (k % kAhead), (k / kAhead) & 1); };
-  auto seg_done = [&](unsigned k) {
+  // Segment k of share x (0: wide, 1 + w: narrow); its place is free again once
+  // every role has said so.
+  auto seg_get = [&](int x, unsigned k) { return wait(kSegFull + 8 * (x * kAhead + k % kAhead), (k / kAhead) & 1); };
+  auto seg_done = [&](int x, unsigned k) {
     __syncwarp();
-    if (lane == 0) bar_arrive(sm + kSegEmptied + 8 * (k % kAhead));
+    if (lane == 0) bar_arrive(sm + kSegDone + 8 * (x * kAhead + k % kAhead));
   };
 
   if (warp >= kMmaWarp) {
     fewer_registers<kOtherRegs>();
-    if (warp == kPlanWarp) {
-      // ===================== the list, and the query tiles ===================
-      Cursor cur = {};
-      int left = 0;
-      if (!idle) {
-        cur.start(plan, static_cast<int>(scan[32]), *found, scan[34], scan[33]);
-        left = static_cast<int>(u1 - u0);
-      }
-      __syncwarp();
-      if (lane == 0) bar_arrive(sm + kReady);   // the scratch has been read: the ring may be filled
-      const int me = blockIdx.x;
-      int4 seg0 = make_int4(0, 0, 0, 0), seg1 = seg0;
-      unsigned put = 0;      // segments written
-      bool ended = false;    // the list's end is
-      auto publish = [&]() {
-        if (put >= kAhead && !wait(kSegEmptied + 8 * (put % kAhead), (put / kAhead - 1) & 1)) return false;
-        Seg* const s = reinterpret_cast<Seg*>(smem + kSegAt) + put % kAhead;
-        if (left <= 0) {
+    const int w = warp & 1;
+    if (warp >= kLoadWarp) {
+      // ============================ plan and load ============================
+      Cursor<kPrefix> cur = {};
+      unsigned put = 0;      // segments of the share written
+      bool more = false;     // the cursor stands on one
+      bool ended = false;    // the share's end is written
+      auto begin = [&](int x, const Partition& part, int64_t all, int share) {
+        const int64_t u = part.start(share);
+        cur.end = part.start(share + 1);
+        put = 0;
+        ended = false;
+        if (kMode == kWindow && lane == 0) {
+          int4* const parts = work.parts + (x == 0 ? 0 : 2 * kMaxCtas) + 2 * share;
+          parts[0] = parts[1] = make_int4(0, 0, 0, 0);
+        }
+        more = !bad && u < cur.end && u < all;
+        if (more) {
+          const Found& f = found[x];
+          cur.start(plan, x == 0, f.v, f.s, f.per_head, f.r, u);
+          more = cur.units() > 0;
+        }
+      };
+      // Writes the next segment of share x, or its end.
+      auto publish = [&](int x, const Partition& part, int share) {
+        const int place = x * kAhead + put % kAhead;
+        if (put >= kAhead && !wait(kSegDone + 8 * place, (put / kAhead - 1) & 1)) return false;
+        Seg* const s = reinterpret_cast<Seg*>(smem + kSegAt) + place;
+        if (!more) {
           if (lane == 0) s->units = 0;
           ended = true;
         } else {
-          const int units = min(cur.n - cur.j, left), row = cur.s.q0 + cur.t * kWideQ;
+          const bool wide = x == 0, own = kPrefix && cur.v >= plan.groups;
+          const int units = cur.units();
           const bool begins = cur.j == 0, ends = cur.j + units == cur.n;
+          const int flags = (cur.empty ? kSegEmpty : 0) | (cur.tiles > 1 ? kSegAgain : 0) |
+                            (kPrefix && !own ? kSegGroup : 0) | (begins && ends ? kSegWhole : 0) |
+                            (own && cur.v - plan.groups >= grouped ? kSegAlone : 0);
           if (lane == 0) {
             s->units = units;
-            s->flags = (cur.cnt > kHalfQ ? kSegWide : 0) | (cur.empty ? kSegEmpty : 0) | (cur.tiles > 1 ? kSegAgain : 0) |
-                       (plan.prefix_mode && cur.v < plan.groups ? kSegGroup : 0) | (begins && ends ? kSegWhole : 0);
+            s->flags = flags;
             s->j0 = cur.j;
             s->cnt = cur.cnt;
-            s->row = row;
+            s->row = cur.row(wide);
             s->head = cur.g * kGroup;
             s->first = cur.first;
             s->low = cur.low;
             int f0 = 0, f1 = 0, f2 = -1;
-            if (plan.prefix_mode) {
+            if (kPrefix) {
               f0 = cur.s.len / kChunkTokens;
             } else if (!cur.empty) {
               f0 = min(cur.first, plan.sinks / kChunkTokens);
@@ -682,86 +880,42 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             s->f2 = f2;
             s->p0 = cur.p0;
             s->len = cur.s.len;
+            s->share = share;
+            s->index = put;
+            s->all = cur.n;
             s->g = cur.g;
             s->table = cur.s.table;
             s->ident = cur.s.ident;
           }
-          // What the merge has to know.
-          if (plan.prefix_mode) {
-            if (lane < cur.cnt) {
-              int* at = work.ends + (cur.v < plan.groups ? 0 : 2 * kNumKVHeads * plan.B) + (row + lane) * kNumKVHeads + cur.g;
-              if (begins) at[0] = me | (put ? kEndSlot : 0) | (lane << kEndPlace) | (ends ? kEndWhole : 0);
-              if (ends) at[kNumKVHeads * plan.B] = me;
+          if (!kPrefix && !(begins && ends)) {
+            const int lo = begins ? share : part.share_of(cur.at + kTileCost);
+            const int hi = ends ? share : part.share_of(cur.at + kTileCost + cur.n - 1);
+            const int slot0 = 2 * lo + (part.start(lo) >= cur.at ? 0 : 1);   // there it may come after other tiles
+            if (lane == 0) {
+              if (kMode == kWindow)
+                work.parts[(x == 0 ? 0 : 2 * kMaxCtas) + 2 * share + (put ? 1 : 0)] =
+                    make_int4(cur.row(wide), cur.g | (cur.cnt << 8), lo | (hi << 16), slot0 + 1);
+              s->lo = lo;
+              s->hi = hi;
+              s->slot0 = slot0;
             }
-          } else if (!(begins && ends)) {
-            const int64_t tile_u = u1 - left - cur.j;   // the tile's first unit
-            const int lo = begins ? me : part.cta_of(tile_u), hi = ends ? me : part.cta_of(tile_u + cur.n - 1);
-            const int4 a = make_int4(row, cur.g | (cur.cnt << 8), lo | (hi << 16), 2 * lo + (part.start(lo) == tile_u ? 0 : 1) + 1);
-            if (put) seg1 = a;
-            else seg0 = a;
           }
-          left -= units;
-          if (left > 0) cur.next(plan);
+          more = cur.next(plan, wide);
         }
         __syncwarp();
-        if (lane == 0) bar_arrive(sm + kSegFull + 8 * (put % kAhead));
+        if (lane == 0) bar_arrive(sm + kSegFull + 8 * place);
         ++put;
         return true;
       };
-      bool ok = true;
-      unsigned loads = 0;
-      // One place stays free: in segment k the planner writes segment k + 7 where
-      // k - 1 was, which does not hold back the query tile of k + 1.
-      for (int i = 0; ok && i < kAhead - 1 && !ended; ++i) ok = publish();
-      for (unsigned k = 0; ok; ++k) {
-        const Seg& s = segs[k % kAhead];
-        const int units = s.units, cnt = s.cnt, row = s.row, head = s.head;
-        if (units == 0) break;
-        if (k) ok = wait(kQEmpty, (k - 1) & 1);
-        if (!ok) break;
-        ++loads;
-        if (lane == 0) {
-          const uint32_t bar = sm + kQFull, q = sm + kQAt;
-          if (cnt == 1) {   // 8 rows; what the other rows of the tile hold is not read back
-            bar_expect(bar, 2 * kGroup * 128);
-            load_box(q, &tm_q1, 0, head, row, bar);
-            load_box(q + kQBoxBytes, &tm_q1, 64, head, row, bar);
-          } else {
-            const int halves = cnt > kHalfQ ? 2 : 1;
-            bar_expect(bar, halves * kQTileBytes);
-            for (int w = 0; w < halves; ++w) {
-              load_box(q + w * kQTileBytes, &tm_q, 0, head, row + w * kHalfQ, bar);
-              load_box(q + w * kQTileBytes + kQBoxBytes, &tm_q, 64, head, row + w * kHalfQ, bar);
-            }
-          }
-        }
-        __syncwarp();
-        if (!ended) ok = publish();
-      }
-      if (!plan.prefix_mode && lane < 2) work.seg[2 * me + lane] = lane ? seg1 : seg0;
-      if (!ok && lane == 0 && loads) {   // a tile in flight lands before the CTA ends
-        volatile int never = 0;
-        mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kQFull), (loads - 1) & 1, &never);
-      }
-    } else if (warp == kLoadWarp) {
-      // ========================== K and V of the units =======================
       const uint64_t policy_once = l2_policy_evict_first(), policy_again = l2_policy_evict_normal();
       const int beyond = static_cast<int>(plan.n_slots) * (kNumKVHeads * kChunkTokens);   // reads as zeros
-      unsigned it = 0;
-      bool ok = wait(kReady, 0);
-      for (unsigned k = 0; ok; ++k) {
-        ok = seg_get(k);
-        if (!ok) break;
-        const Seg& s = segs[k % kAhead];
-        const int units = s.units, flags = s.flags, j0 = s.j0, first = s.first, low = s.low, g = s.g;
-        const int32_t* const table = s.table;
-        const int64_t ident = s.ident;
-        seg_done(k);
-        if (units == 0) break;
-        // Another tile of the list reads the same chunks: they stay in L2.
+      // K and V of a segment's units, which are units x .. of the share.
+      auto load_units = [&](const Ring& ring, unsigned x, int units, int flags, int j0, int first, int low, int g,
+                            const int32_t* table, int64_t ident) {
+        // Another tile of the entry reads the same chunks: they stay in L2.
         const uint64_t policy = (flags & kSegAgain) ? policy_again : policy_once;
         int row = 0;
-        for (int i = 0; i < units; ++i, ++it) {
+        for (int i = 0; i < units; ++i, ++x) {
           if ((i & 31) == 0) {   // the rows of 32 units at a time, a lane each
             row = beyond;
             if (!(flags & kSegEmpty) && i + lane < units) {
@@ -774,87 +928,176 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
           }
           const int y = __shfl_sync(0xffffffffu, row, i & 31);
-          const int st = it % kStages;
-          if (it >= kStages) ok = wait(kEmpty + 8 * st, (it / kStages - 1) & 1);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t dst = sm + st * kStageBytes, bar = sm + kFull + 8 * st;
-            bar_expect(bar, kStageBytes);
-            load_box(dst, &tm_k, 0, y, bar, policy);
-            load_box(dst + kBoxBytes, &tm_k, 64, y, bar, policy);
-            load_box(dst + 2 * kBoxBytes, &tm_v, 0, y, bar, policy);
-            load_box(dst + 3 * kBoxBytes, &tm_v, 64, y, bar, policy);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const unsigned h = ring.half(2 * x + kv);
+            // The use before this one has been read (a half's first use needs no wait).
+            if ((2 * x + kv > ring.mask || ((ring.used >> h) & 1)) && !wait(kEmpty + 8 * h, ring.parity(2 * x + kv) ^ 1)) return false;
+            if (lane == 0) {
+              const uint32_t dst = sm + h * kHalfBytes, bar = sm + kFull + 8 * h;
+              const CUtensorMap* const map = kv ? &tm_v : &tm_k;
+              bar_expect(bar, kHalfBytes);
+              load_box(dst, map, 0, y, bar, policy);
+              load_box(dst + kBoxBytes, map, 64, y, bar, policy);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
+        return true;
+      };
+      bool ok = true;
+      unsigned wide_units = 0;
+      if (!kHasWide) {
+      } else if (warp == kLoadWarp) {
+        for (unsigned k = 0; ok; ++k) {
+          ok = seg_get(0, k);
+          if (!ok) break;
+          const Seg& s = segs[k % kAhead];
+          const int units = s.units, flags = s.flags, j0 = s.j0, first = s.first, low = s.low, g = s.g;
+          const int32_t* const table = s.table;
+          const int64_t ident = s.ident;
+          seg_done(0, k);
+          if (units == 0) break;
+          ok = load_units(wide_ring(), wide_units, units, flags, j0, first, low, g, table, ident);
+          wide_units += units;
+        }
+        if (ok && lane == 0) bar_arrive(sm + kHandOver + 8);
+        if (ok) ok = wait(kHandOver, 0);
+      } else {
+        begin(0, part_w, total[1], me);
+        // One place stays free: in segment k the planner writes segment k + 3
+        // where k - 1 was, which does not hold back the query tiles of k + 1.
+        ok = publish(0, part_w, me);
+        unsigned k = 0;
+        for (; ok; ++k) {
+          const Seg& s = segs[k % kAhead];
+          const int units = s.units, cnt = s.cnt, row = s.row, head = s.head;
+          if (units == 0) break;
+          wide_units += units;
+          for (int t = 0; ok && t < 2; ++t) {   // a pipeline's half of the queries each
+            if (k) ok = wait(kQEmpty + 8 * t, (k - 1) & 1);
+            if (ok && lane == 0) {
+              const uint32_t bar = sm + kQFull + 8 * t, q = sm + kQAt + t * kQTileBytes;
+              const int at = row + (t ? (cnt + 1) >> 1 : 0);
+              bar_expect(bar, kQTileBytes);
+              load_box(q, &tm_q16, 0, head, at, bar);
+              load_box(q + kQBoxBytes, &tm_q16, 64, head, at, bar);
+            }
+            __syncwarp();
+          }
+          while (ok && !ended && put < k + kAhead) ok = publish(0, part_w, me);
+        }
+        for (int t = 0; ok && k && t < 2; ++t) ok = wait(kQEmpty + 8 * t, (k - 1) & 1);
+        if (ok && lane == 0) bar_arrive(sm + kHandOver);
+        if (ok) ok = wait(kHandOver + 8, 0);
+        if (!ok && lane == 0 && k) {   // tiles in flight land before the CTA ends
+          volatile int never = 0;
+          for (int t = 0; t < 2; ++t)
+            mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kQFull) + t, (k - 1) & 1, &never);
+        }
+      }
+      // The pipeline's narrow share.
+      const Ring ring = narrow_ring(w, wide_units);
+      unsigned x = 0, loads = 0;
+      if (ok) begin(1 + w, part_n, total[0], 2 * me + w);
+      for (unsigned k = 0; ok; ++k) {
+        const int units = more ? cur.units() : 0, cnt = cur.cnt, row = cur.row(false), j0 = cur.j, first = cur.first,
+                  low = cur.low, g = cur.g, flags = cur.empty ? kSegEmpty : 0;
+        const int32_t* const table = cur.s.table;
+        const int64_t ident = cur.s.ident;
+        ok = publish(1 + w, part_n, 2 * me + w);
+        if (!ok || units == 0) break;
+        const int b = k & 1;
+        if (k >= 2) ok = wait(kNEmpty + 16 * w + 8 * b, ((k >> 1) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t bar = sm + kNFull + 16 * w + 8 * b, q = sm + kQAt + w * kQTileBytes + b * kQ2Bytes;
+          const CUtensorMap* const map = cnt == 1 ? &tm_q1 : &tm_q8;   // what other rows hold is not read back
+          bar_expect(bar, 2 * 128 * kGroup * (cnt == 1 ? 1 : kNarrowQ));
+          load_box(q, map, 0, g * kGroup, row, bar);
+          load_box(q + kQBoxBytes, map, 64, g * kGroup, row, bar);
+        }
+        __syncwarp();
+        ++loads;
+        ok = load_units(ring, x, units, flags, j0, first, low, g, table, ident);
+        x += units;
       }
       if (!ok && lane == 0) {   // copies in flight land before the CTA ends
         volatile int never = 0;
-        for (unsigned i = it > kStages ? it - kStages : 0; i < it; ++i)
-          mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kFull) + i % kStages, (i / kStages) & 1, &never);
+        uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kBarAt);
+        for (unsigned i = loads > 2 ? loads - 2 : 0; i < loads; ++i)
+          mbar_wait_bounded(bars + (kNFull - kBarAt) / 8 + 2 * w + (i & 1), (i >> 1) & 1, &never);
+        const unsigned end = 2 * (loads ? x : wide_units);
+        const Ring r = loads ? ring : wide_ring();
+        for (unsigned i = end > r.mask ? end - r.mask - 1 : 0; i < end; ++i)
+          if (loads || warp == kLoadWarp) mbar_wait_bounded(bars + r.half(i), r.parity(i), &never);
       }
     } else {
       // =============================== products ==============================
-      // A warp for each softmax warpgroup: the issue of one's products, and its
-      // waits, run beside the other's.  The whole warp walks the segments (its
-      // values stay uniform) and one lane issues.
-      const int w = warp - kMmaWarp;
+      // The whole warp walks the segments (its values stay uniform) and one lane
+      // issues.
       const uint32_t leader = elect_one() ? 1u : 0u;
-      const uint32_t k_lo0 = desc_lo_kmajor(sm), v_lo0 = desc_lo_v(sm + 2 * kBoxBytes), q_lo0 = desc_lo_kmajor(sm + kQAt);
+      const uint32_t k_lo0 = desc_lo_kmajor(sm), v_lo0 = desc_lo_v(sm), q_lo0 = desc_lo_kmajor(sm + kQAt + w * kQTileBytes);
       const uint32_t o_acc = tmem + kOCol0 + w * kHeadDim, s_col0 = tmem + 2 * w * kSCols;
       const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
-      unsigned it = 0, job = 0;   // units, and units of this warpgroup so far
+      unsigned job = 0, wide_units = 0;   // units so far, of them in the wide share
       bool ok = true;
-      for (unsigned k = 0; ok; ++k) {
-        ok = seg_get(k);
-        if (!ok) break;
-        const int n = segs[k % kAhead].units;
-        const bool wide = segs[k % kAhead].flags & kSegWide;
-        seg_done(k);
-        if (n == 0) break;
-        const int mine = wide ? n : (n + 1 - w) >> 1;   // units of this warpgroup: all, or every other one
-        const unsigned step = wide ? 1 : 2, at0 = it + (wide ? 0 : w);
-        const uint32_t q_lo = q_lo0 + (wide ? w * (kQTileBytes >> 4) : 0);
-        ok = wait(kQFull, k & 1);
-        if (ok && !mine && lane == 0) bar_arrive(sm + kQEmpty);
-        // Scores run up to two units (both buffers) before the products, as far
-        // as units have arrived: waiting for one that has not would hold back the
-        // product that frees a stage.
-        int next = 0;
-        for (int i = 0; ok && i < mine; ++i) {
-          for (; next < min(mine, i + 2); ++next) {
-            const unsigned at = at0 + next * step, st = at % kStages, x = job + next, buf = x & 1;
-            if (next > i) {
-              if (!__all_sync(0xffffffffu, bar_try(sm + kFull + 8 * st, (at / kStages) & 1))) break;
-            } else {
-              ok = wait(kFull + 8 * st, (at / kStages) & 1);
+#pragma unroll 1
+      for (int x = kHasWide ? 0 : 1 + w; ok && x <= 1 + w; x += 1 + w) {   // the wide share, then the narrow one
+        const Ring ring = x == 0 ? wide_ring() : narrow_ring(w, wide_units);
+        unsigned at = 0;   // units of the share so far
+        for (unsigned k = 0; ok; ++k) {
+          ok = seg_get(x, k);
+          if (!ok) break;
+          const int n = segs[x * kAhead + k % kAhead].units;
+          seg_done(x, k);
+          if (n == 0) break;
+          const int q_full = x == 0 ? kQFull + 8 * w : kNFull + 16 * w + 8 * (k & 1);
+          const int q_empty = x == 0 ? kQEmpty + 8 * w : kNEmpty + 16 * w + 8 * (k & 1);
+          const uint32_t q_lo = q_lo0 + (x == 0 ? 0 : (k & 1) * (kQ2Bytes >> 4));
+          ok = wait(q_full, (x == 0 ? k : k >> 1) & 1);
+          // Scores run up to two units (both buffers) before the products, as far
+          // as units have arrived: waiting for one that has not would hold back
+          // the product that frees a half-stage.
+          int next = 0;
+          for (int i = 0; ok && i < n; ++i) {
+            for (; next < min(n, i + 2); ++next) {
+              const unsigned kx = 2 * (at + next), h = ring.half(kx), jb = job + next, buf = jb & 1;
+              if (next > i) {
+                if (!__all_sync(0xffffffffu, bar_try(sm + kFull + 8 * h, ring.parity(kx)))) break;
+              } else {
+                ok = wait(kFull + 8 * h, ring.parity(kx));
+              }
+              if (ok && jb >= 2) ok = wait(o_bar + 8 * buf, ((jb - 2) >> 1) & 1);   // the buffer's probabilities are read
+              if (!ok) break;
+              tcgen05_fence_after();
+              const uint32_t k_lo = k_lo0 + h * (kHalfBytes >> 4), d = s_col0 + buf * kSCols;
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                mma_ss(leader, d, q_lo + (y >> 2) * (kQBoxBytes >> 4) + (y & 3) * 2,
+                       k_lo + (y >> 2) * (kBoxBytes >> 4) + (y & 3) * 2, kIdescS, y > 0);
+              mma_commit(leader, sm + s_bar + 8 * buf);
+              mma_commit(leader, sm + kEmpty + 8 * h);
+              if (x) mma_commit(leader, sm + kEmpty + 8 * h);
+              if (next == n - 1) mma_commit(leader, sm + q_empty);
             }
-            if (ok && x >= 2) ok = wait(o_bar + 8 * buf, ((x - 2) >> 1) & 1);   // the buffer's probabilities are read
+            if (!ok) break;
+            const unsigned vx = 2 * (at + i) + 1, h = ring.half(vx), jb = job + i, buf = jb & 1;
+            ok = wait(kFull + 8 * h, ring.parity(vx)) && wait(p_bar + 8 * buf, (jb >> 1) & 1);
             if (!ok) break;
             tcgen05_fence_after();
-            const uint32_t k_lo = k_lo0 + st * (kStageBytes >> 4), d = s_col0 + buf * kSCols;
+            const uint32_t v_lo = v_lo0 + h * (kHalfBytes >> 4), a = s_col0 + buf * kSCols;
 #pragma unroll
-            for (int x8 = 0; x8 < 8; ++x8)
-              mma_ss(leader, d, q_lo + (x8 >> 2) * (kQBoxBytes >> 4) + (x8 & 3) * 2,
-                     k_lo + (x8 >> 2) * (kBoxBytes >> 4) + (x8 & 3) * 2, kIdescS, x8 > 0);
-            mma_commit(leader, sm + s_bar + 8 * buf);
-            if (next == mine - 1) mma_commit(leader, sm + kQEmpty);
+            for (int y = 0; y < 4; ++y)
+              mma_ts(leader, o_acc, a + 8 * y, v_lo + y * (2048 >> 4), kIdescO, y > 0 || i > 0);
+            mma_commit(leader, sm + o_bar + 8 * buf);
+            mma_commit(leader, sm + kEmpty + 8 * h);
+            if (x) mma_commit(leader, sm + kEmpty + 8 * h);
           }
-          if (!ok) break;
-          const unsigned at = at0 + i * step, st = at % kStages, x = job + i, buf = x & 1;
-          ok = wait(p_bar + 8 * buf, (x >> 1) & 1);
-          if (!ok) break;
-          tcgen05_fence_after();
-          const uint32_t v_lo = v_lo0 + st * (kStageBytes >> 4), a = s_col0 + buf * kSCols;
-#pragma unroll
-          for (int x4 = 0; x4 < 4; ++x4)
-            mma_ts(leader, o_acc, a + 8 * x4, v_lo + x4 * (2048 >> 4), kIdescO, x4 > 0 || i > 0);
-          mma_commit(leader, sm + o_bar + 8 * buf);
-          mma_commit(leader, sm + kEmpty + 8 * st);
-          if (!wide) mma_commit(leader, sm + kEmpty + 8 * st);
+          job += n;
+          at += n;
         }
-        job += mine;
-        it += n;
+        if (x == 0) wide_units = at;
       }
       mma_commit(leader, sm + kDrain + 8 * w);   // every product has ended before TMEM is given back
       volatile int never = 0;
@@ -864,329 +1107,296 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     // ================================= softmax ================================
     more_registers<kSoftmaxRegs>();
     const int w = warp >> 2, wq = warp & 3;
-    const int r = wq * 32 + lane;                    // row of the tile
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_col0 = tmem + 2 * w * kSCols + lanes, o_mine = tmem + kOCol0 + w * kHeadDim + lanes;
+    const uint32_t s_col0 = tmem + 2 * w * kSCols + lanes, o_col0 = tmem + kOCol0 + w * kHeadDim + lanes;
     const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
     const uint64_t scale2 = pack2(scale_log2, scale_log2);
-    unsigned job0 = 0, job1 = 0, it = 0, joins = 0;
+    unsigned job = 0, wide_units = 0;
     bool ok = true;
-    // Both warpgroups.
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) bar_arrive(sm + kMeet);
-      return wait(kMeet, joins++ & 1);
-    };
-    for (unsigned k = 0; ok; ++k) {
-      ok = seg_get(k);
-      if (!ok) break;
-      const Seg& sg = segs[k % kAhead];
-      const int n = sg.units, j0 = sg.j0, f0 = sg.f0 - j0, f1 = sg.f1 - j0, f2 = sg.f2 - j0;
-      if (n == 0) break;
-      const bool wide = sg.flags & kSegWide;
-      const int rows = kGroup * (wide ? (w == 0 ? kHalfQ : sg.cnt - kHalfQ) : sg.cnt);   // of this warpgroup
-      const bool active = wq * 32 < rows;            // the warp has rows
-      float m = -INFINITY, l = 0.f;
-      const unsigned job_first = w ? job1 : job0;
-      unsigned job = job_first;
-      for (int i = wide ? 0 : w; i < n; i += wide ? 1 : 2, ++job) {
-        const unsigned buf = job & 1;
-        uint64_t see = ~0ull;                        // tokens of the unit that this row sees
-        const bool edge = !(i < f0 || (i >= f1 && i <= f2));
-        ok = wait(s_bar + 8 * buf, (job >> 1) & 1);
+#pragma unroll 1
+    for (int share = kHasWide ? 0 : 1 + w; ok && share <= 1 + w; share += 1 + w) {
+      const bool wide = share == 0;
+      unsigned at = 0;
+      for (unsigned k = 0; ok; ++k) {
+        ok = seg_get(share, k);
         if (!ok) break;
-        tcgen05_fence_after();
-        if (edge) {
-          uint64_t any;                              // tokens that some query of the tile sees
-          const int j = j0 + i, kb = (j < sg.first ? j : sg.low + j - sg.first) * kChunkTokens;
-          if (sg.flags & kSegEmpty) {
-            any = see = 0;
-          } else if (plan.prefix_mode) {
-            any = see = lowest(sg.len - kb);
-          } else {
-            const int pos = sg.p0 + (wide ? w * kHalfQ : 0) + (r >> 3) - kb;   // of the row's query, in the unit
-            any = lowest(sg.p0 + sg.cnt - kb) & (~lowest(sg.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
-            see = lowest(pos + 1) & (~lowest(pos - plan.window + 1) | lowest(plan.sinks - kb));
-          }
-          if (any != ~0ull) {
-            // Unseen rows of V become zeros (their probabilities are zero, what
-            // the page holds there may not be finite).  Both warpgroups of a wide
-            // tile write the same zeros.
-            const unsigned at = it + i, st = at % kStages;
-            ok = wait(kFull + 8 * st, (at / kStages) & 1);
-            if (!ok) break;
-            uint8_t* vs = smem + st * kStageBytes + 2 * kBoxBytes;
-            for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
-              const int row = x >> 4;
-              if (!((any >> row) & 1))
-                *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-        }
-        if (active) {
-          const uint32_t sp = s_col0 + buf * kSCols;
-          float s[64];
-          tmem_ld32(sp, s);
-          tmem_ld32(sp + 32, s + 32);
-          tmem_wait_ld(s, 64);
+        const Seg& sg = segs[share * kAhead + k % kAhead];
+        const int n = sg.units, j0 = sg.j0, f0 = sg.f0 - j0, f1 = sg.f1 - j0, f2 = sg.f2 - j0;
+        if (n == 0) break;
+        // The warp's queries: i_first .. of the tile, 4 at most.
+        const int half = (sg.cnt + 1) >> 1;
+        const int i_first = (wide && w ? half : 0) + 4 * wq;
+        const int queries = min(4, (wide && !w ? half : sg.cnt) - i_first);
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const unsigned buf = (job + i) & 1;
+          uint64_t see = ~0ull;                      // tokens of the unit that this row sees
+          const bool edge = !(i < f0 || (i >= f1 && i <= f2));
+          ok = wait(s_bar + 8 * buf, ((job + i) >> 1) & 1);
+          if (!ok) break;
+          tcgen05_fence_after();
           if (edge) {
-            const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
+            uint64_t any;                            // tokens that some query of the tile sees
+            const int j = j0 + i, kb = (j < sg.first ? j : sg.low + j - sg.first) * kChunkTokens;
+            if (sg.flags & kSegEmpty) {
+              any = see = 0;
+            } else if (kPrefix) {
+              any = see = lowest(sg.len - kb);
+            } else {
+              const int pos = sg.p0 + i_first + (lane >> 3) - kb;   // of the row's query, in the unit
+              any = lowest(sg.p0 + sg.cnt - kb) & (~lowest(sg.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
+              see = lowest(pos + 1) & (~lowest(pos - plan.window + 1) | lowest(plan.sinks - kb));
+            }
+            if (any != ~0ull) {
+              // Unseen rows of V become zeros (their probabilities are zero, what
+              // the page holds there may not be finite).  Both pipelines write the
+              // same zeros to a wide tile's.
+              const Ring ring = wide ? wide_ring() : narrow_ring(w, wide_units);
+              const unsigned vx = 2 * (at + i) + 1, h = ring.half(vx);
+              ok = wait(kFull + 8 * h, ring.parity(vx));
+              if (!ok) break;
+              uint8_t* const vs = smem + h * kHalfBytes;
+              for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
+                const int row = x >> 4;
+                if (!((any >> row) & 1))
+                  *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+            }
+          }
+          if (queries > 0) {
+            const uint32_t sp = s_col0 + buf * kSCols;
+            float s[64];
+            tmem_ld32(sp, s);
+            tmem_ld32(sp + 32, s + 32);
+            tmem_wait_ld(s, 64);
+            if (edge) {
+              const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                if (!((see0 >> c) & 1)) s[c] = -INFINITY;
+                if (!((see1 >> c) & 1)) s[c + 32] = -INFINITY;
+              }
+            }
+            float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
+#pragma unroll
+            for (int c = 12; c < 60; c += 8) {
+              mx[0] = max3(mx[0], s[c], s[c + 1]);
+              mx[1] = max3(mx[1], s[c + 2], s[c + 3]);
+              mx[2] = max3(mx[2], s[c + 4], s[c + 5]);
+              mx[3] = max3(mx[3], s[c + 6], s[c + 7]);
+            }
+            mx[0] = max3(mx[0], s[60], s[61]);
+            mx[1] = max3(mx[1], s[62], s[63]);
+            const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
+            const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;   // a row's first score that is not masked always does
+            if (__any_sync(0xffffffffu, raise)) {
+              const float m_new = raise ? top : m;
+              const float f = raise ? fast_exp2(m - m_new) : 1.f;
+              m = m_new;
+              l *= f;
+              if (i > 0) {                           // the accumulator of earlier units follows
+                ok = wait(o_bar + 8 * (buf ^ 1), ((job + i - 1) >> 1) & 1);
+                if (!ok) break;
+                tcgen05_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < kHeadDim; c += 32) {
+                  float o[32];
+                  tmem_ld32(o_col0 + c, o);
+                  tmem_wait_ld(o, 32);
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) o[x] *= f;
+                  tmem_st32(o_col0 + c, o);
+                }
+              }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every probability is 0
+            const uint64_t ref2 = pack2(-ref, -ref);
+            uint64_t sum[4] = {0, 0, 0, 0};
+            float pk[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              if (!((see0 >> c) & 1)) s[c] = -INFINITY;
-              if (!((see1 >> c) & 1)) s[c + 32] = -INFINITY;
+              float a, b;
+              const uint64_t x = fma2(pack2(s[2 * c], s[2 * c + 1]), scale2, ref2);
+              if (c % kFmaEvery == kFmaEvery - 1) {
+                exp2_fma(x, a, b);
+              } else {
+                unpack2(x, a, b);
+                a = fast_exp2(a);
+                b = fast_exp2(b);
+              }
+              sum[c & 3] = add2(sum[c & 3], pack2(a, b));
+              // One rounding of the probabilities to bf16, half a step (2^-9) at
+              // most: the output is rounded to the same type.
+              pk[c] = __uint_as_float(pack_bf16(a, b));
             }
+            tmem_st32(sp, pk);
+            float sa, sb;
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), sa, sb);
+            l += sa + sb;
+            tmem_wait_st();
           }
-          float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
-#pragma unroll
-          for (int c = 12; c < 60; c += 8) {
-            mx[0] = max3(mx[0], s[c], s[c + 1]);
-            mx[1] = max3(mx[1], s[c + 2], s[c + 3]);
-            mx[2] = max3(mx[2], s[c + 4], s[c + 5]);
-            mx[3] = max3(mx[3], s[c + 6], s[c + 7]);
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(sm + p_bar + 8 * buf);
+        }
+        if (!ok) break;
+
+        // ---- the end of a segment: the output of a whole tile, or a partial ----
+        job += n;
+        at += n;
+        ok = wait(o_bar + 8 * ((job - 1) & 1), ((job - 1) >> 1) & 1);   // its commit follows all earlier products
+        if (!ok) break;
+        tcgen05_fence_after();
+        if (queries > 0) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          // Where the rows go: 128 bytes of a row per 8 lanes.  A thread holds a
+          // row, so the rows turn in the warp's 4 KiB of shared memory, 16-byte
+          // piece x of row y at place x ^ (y % 8) (no bank conflicts either way).
+          const bool whole = sg.flags & kSegWhole, final = whole && (!kPrefix || (sg.flags & kSegAlone));
+          const int row0 = sg.row + i_first, head = sg.head;
+          // Output rows: (query, head); a record's: the same, a tile at a time.
+          const int64_t out_row = static_cast<int64_t>(row0) * kNumQHeads + head;
+          const int64_t places = static_cast<int64_t>(kNumQHeads) * plan.B;
+          int64_t rec = out_row;
+          int q_rows = kNumQHeads;                   // rows from a query to the next
+          if (whole) {
+            if (!(sg.flags & kSegGroup)) rec += places;   // (prefix mode; a window's whole tile is final)
+          } else {
+            rec = work.slots[wide] + (2ll * sg.share + (sg.index > 0)) * work.rows[wide] + i_first * kGroup;
+            q_rows = kGroup;
           }
-          mx[0] = max3(mx[0], s[60], s[61]);
-          mx[1] = max3(mx[1], s[62], s[63]);
-          const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
-          const bool raise = !(top <= m + kRaise) && r < rows;   // a row's first score that is not masked always does
-          if (__any_sync(0xffffffffu, raise)) {
-            const float m_new = raise ? top : m;
-            const float f = raise ? fast_exp2(m - m_new) : 1.f;
-            m = m_new;
-            l *= f;
-            if (job != job_first) {                  // the accumulator of earlier units follows
-              ok = wait(o_bar + 8 * (buf ^ 1), ((job - 1) >> 1) & 1);
-              if (!ok) break;
-              tcgen05_fence_after();
+          uint8_t* const mine = smem + kTurnAt + warp * kTurnBytes;
+          uint8_t* const row_at = mine + lane * 128;
+          // fp32 records go 32 columns at a time, bf16 outputs 64.
+          uint8_t* to = final ? reinterpret_cast<uint8_t*>(out + out_row * kHeadDim)
+                              : reinterpret_cast<uint8_t*>(work.o + rec * kHeadDim);
+          const int row_bytes = final ? 2 * kHeadDim : 4 * kHeadDim;
 #pragma unroll 1
-              for (int c = 0; c < kHeadDim; c += 32) {
-                float o[32];
-                tmem_ld32(o_mine + c, o);
-                tmem_wait_ld(o, 32);
+          for (int c = 0; c < kHeadDim; c += 32) {
+            float o[32];
+            tmem_ld32(o_col0 + c, o);
+            tmem_wait_ld(o, 32);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= f;
-                tmem_st32(o_mine + c, o);
+            for (int x = 0; x < 32; ++x) o[x] *= inv;
+            if (final) {
+              const int z = (c >> 3) & 4;
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                               pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
+              if (!z) continue;
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                *reinterpret_cast<float4*>(row_at + ((x ^ (lane & 7)) << 4)) =
+                    make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int y = 4 * x + (lane >> 3);     // row of the warp: query y / 8, head y % 8
+              if ((y >> 3) < queries)
+                *reinterpret_cast<uint4*>(to + ((y >> 3) * q_rows + (y & 7)) * row_bytes + (lane & 7) * 16) =
+                    *reinterpret_cast<const uint4*>(mine + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+            }
+            __syncwarp();
+            to += 128;
+          }
+          tcgen05_fence_before();
+          if (!final) {
+            if ((lane >> 3) < queries)
+              work.lse[rec + (lane >> 3) * q_rows + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
+            if (kFold) {
+              // Few queries a sequence: the warp that adds a tile's last units
+              // folds its rows (the other shares' are from the same warp there).
+              int* const count = work.count + sg.lo * 2 + wq;
+              int before = 0;
+              __threadfence();
+              __syncwarp();
+              if (lane == 0) before = atomicAdd(count, n);
+              if (__shfl_sync(0xffffffffu, before, 0) + n == sg.all) {
+                if (lane == 0) *count = 0;
+                __threadfence();
+                const int lo = sg.lo, slot0 = sg.slot0, rows = work.rows[0];
+                for (int i = 0; i < queries; ++i) {
+                  const int64_t at0 = work.slots[0] + (i_first + i) * kGroup;
+                  fold_query(work, sg.hi - lo + 1, lane,
+                             [&](int x) -> int64_t { return at0 + static_cast<int64_t>(x == 0 ? slot0 : 2 * (lo + x)) * rows; },
+                             out + (out_row + static_cast<int64_t>(i) * kNumQHeads) * kHeadDim);
+                }
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every probability is 0
-          const uint64_t ref2 = pack2(-ref, -ref);
-          uint64_t sum[4] = {0, 0, 0, 0};
-          float pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float a, b;
-            const uint64_t x = fma2(pack2(s[2 * c], s[2 * c + 1]), scale2, ref2);
-            if (c % kFmaEvery == kFmaEvery - 1) {
-              exp2_fma(x, a, b);
-            } else {
-              unpack2(x, a, b);
-              a = fast_exp2(a);
-              b = fast_exp2(b);
-            }
-            sum[c & 3] = add2(sum[c & 3], pack2(a, b));
-            // One rounding of the probabilities to bf16, half a step (2^-9) at
-            // most: the output is rounded to the same type.
-            pk[c] = __uint_as_float(pack_bf16(a, b));
+          if (kPrefix && lane < queries) {   // where the merge finds the partials
+            const int part = (sg.flags & kSegGroup) ? 0 : 2, pairs = plan.B * kNumKVHeads;
+            int* const ends = work.ends + (row0 + lane) * kNumKVHeads + (head >> 3);
+            if (j0 == 0)
+              ends[part * pairs] = final ? kNone
+                                         : sg.share | (sg.index > 0 ? kEndSlot : 0) | (wide ? kEndWide : 0) |
+                                               ((i_first + lane) << kEndPlace) | (whole ? kEndWhole : 0);
+            if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.share;
+            if (sg.flags & kSegAlone) ends[0] = kNone;
           }
-          tmem_st32(sp, pk);
-          float sa, sb;
-          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), sa, sb);
-          l += sa + sb;
-          tmem_wait_st();
         }
         tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(sm + p_bar + 8 * buf);
+        seg_done(share, k);
       }
-      if (!ok) break;
-
-      // ---- the end of a segment: the tile's output, or this CTA's partial ----
-      const unsigned n0 = wide ? n : (n + 1) >> 1, n1 = wide ? n : n >> 1;
-      const unsigned last0 = job0 + n0 - 1, last1 = job1 + n1 - 1;
-      float* const ml = reinterpret_cast<float*>(smem + kMlAt);   // [2 warpgroups][m, l][128 rows]
-      if (!wide) {
-        ml[2 * w * 128 + r] = m;
-        ml[(2 * w + 1) * 128 + r] = l;
-        ok = meet();   // both have their last scores: the waits below name each barrier's next phase
-      }
-      // The last product of a warpgroup (its commit follows all earlier ones).
-      if (ok && (!wide || w == 0)) ok = wait(kODone + 8 * (last0 & 1), (last0 >> 1) & 1);
-      if (ok && (wide ? w == 1 : n1 > 0)) ok = wait(kODone + 16 + 8 * (last1 & 1), (last1 >> 1) & 1);
-      if (!ok) break;
-      tcgen05_fence_after();
-      float part0 = 1.f, part1 = 0.f;
-      if (!wide) {
-        const float m0 = ml[r], l0 = ml[128 + r], m1 = ml[256 + r], l1 = ml[384 + r];
-        m = fmaxf(m0, m1);
-        const float ref = m == -INFINITY ? 0.f : m;
-        part0 = fast_exp2(m0 - ref);
-        part1 = fast_exp2(m1 - ref);
-        l = l0 * part0 + l1 * part1;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      part0 *= inv;
-      part1 *= inv;
-      // Where the rows go: 128 bytes of a row per 8 lanes.  A thread holds a row,
-      // so the rows turn in the warp's 4 KiB of shared memory, 16-byte piece x of
-      // row y at place x ^ (y % 8) (no bank conflicts either way).
-      if (active) {
-        const bool whole = sg.flags & kSegWhole, final = whole && !plan.prefix_mode;
-        const int q_first = (wide ? w * kHalfQ : 0) + wq * 4;   // the warp's first query in the tile
-        // Output rows: (query, head); a record's: the same, a tile at a time.
-        const int64_t out_row = (static_cast<int64_t>(sg.row) + q_first) * kNumQHeads + sg.head;
-        int64_t rec = out_row;
-        int q_rows = kNumQHeads;                                // rows from a query to the next
-        if (plan.prefix_mode && whole) {
-          rec += (sg.flags & kSegGroup) ? 0 : static_cast<int64_t>(kNumQHeads) * plan.B;
-        } else if (!final) {
-          rec = (plan.prefix_mode ? 2ll * kNumQHeads * plan.B : 0) + (2ll * blockIdx.x + (k > 0)) * work.rows_cap +
-                q_first * kGroup;
-          q_rows = kGroup;
-        }
-        uint8_t* const mine = smem + kTurnAt + warp * kTurnBytes;
-        uint8_t* const row_at = mine + lane * 128;
-        // fp32 records go 32 columns at a time, bf16 outputs 64.
-        const int c_lo = wide ? 0 : 64 * w, c_hi = wide ? kHeadDim : 64 * w + 64;
-        uint8_t* to = final ? reinterpret_cast<uint8_t*>(out) + (out_row * kHeadDim + c_lo) * 2
-                            : reinterpret_cast<uint8_t*>(work.o + rec * kHeadDim + c_lo);
-        const int row_bytes = final ? 2 * kHeadDim : 4 * kHeadDim;
-#pragma unroll 1
-        for (int c = c_lo; c < c_hi; c += 32) {
-          float o[32];
-          tmem_ld32((wide ? o_mine : tmem + kOCol0 + lanes) + c, o);
-          if (!wide && n1) {
-            float o2[32];
-            tmem_ld32(tmem + kOCol0 + kHeadDim + lanes + c, o2);
-            tmem_wait_ld(o, 32);
-            tmem_wait_ld(o2, 32);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = fmaf(o2[x], part1, o[x] * part0);
-          } else {
-            tmem_wait_ld(o, 32);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= part0;
-          }
-          if (final) {
-            const int z = (c >> 3) & 4;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
-                  make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                             pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-            if (!z) continue;
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<float4*>(row_at + ((x ^ (lane & 7)) << 4)) =
-                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int y = 4 * x + (lane >> 3);   // row of the warp: query y / 8, head y % 8
-            if (wq * 32 + y < rows)
-              *reinterpret_cast<uint4*>(to + ((y >> 3) * q_rows + (y & 7)) * row_bytes + (lane & 7) * 16) =
-                  *reinterpret_cast<const uint4*>(mine + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
-          }
-          __syncwarp();
-          to += 128;
-        }
-        if (!final && r < rows && (wide || w == 0))
-          work.lse[rec + (lane >> 3) * q_rows + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
-      }
-      tcgen05_fence_before();
-      // In a narrow tile each warpgroup reads the other's accumulator: neither
-      // lets the next segment's products start before both have.
-      if (!wide) ok = meet();
-      seg_done(k);
-      job0 += n0;
-      job1 += n1;
-      it += n;
+      if (share == 0) wide_units = at;
     }
   }
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
+  if (tid < 6 && *reinterpret_cast<const volatile int*>(smem + kAbortAt)) {
+    // A wait ran out: what the merge would read may be a former call's.
+    if (kPrefix) *work.ok = 0;
+    else if (!kFold) work.parts[tid < 2 ? 2 * me + tid : 2 * kMaxCtas + 4 * me + tid - 2] = make_int4(0, 0, 0, 0);
+  }
   if (warp == kMmaWarp) {
     tcgen05_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-// ---- folding the partials -----------------------------------------------------
+// ---- the merge kernels --------------------------------------------------------
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 
-// The partials of one row, joined in their order: `row(i)` for i < n.  The loads
-// of 8 partials are issued together.
-struct Fold {
-  float m = -INFINITY, den = 0.f;
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  template <typename Row>
-  __device__ void add(const Work& w, int n, int lane, Row row) {
-    constexpr int kBatch = 8;
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-      float lse[kBatch];
-      uint4 raw[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        lse[i] = -INFINITY;
-        if (i0 + i < n) {
-          const int64_t at = row(i0 + i);
-          lse[i] = ld_dep(w.lse + at);
-          raw[i] = ld_dep(reinterpret_cast<const uint4*>(w.o + at * kHeadDim) + lane);
-        }
-      }
-      float top = m;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, lse[i]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float f = fast_exp2(m - ref);
-      m = top;
-      den *= f;
-      r.x *= f; r.y *= f; r.z *= f; r.w *= f;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (i0 + i < n) {
-          const float wt = fast_exp2(lse[i] - ref);
-          den += wt;
-          r.x = fmaf(wt, __uint_as_float(raw[i].x), r.x);
-          r.y = fmaf(wt, __uint_as_float(raw[i].y), r.y);
-          r.z = fmaf(wt, __uint_as_float(raw[i].z), r.z);
-          r.w = fmaf(wt, __uint_as_float(raw[i].w), r.w);
-        }
-      }
-    }
-  }
-  __device__ void store(__nv_bfloat16* out, int64_t row, int lane) const {   // row: query * 64 + head
-    const float id = den == 0.f ? 0.f : 1.f / den;
-    *reinterpret_cast<uint2*>(out + row * kHeadDim + 4 * lane) =
-        make_uint2(pack_bf16(r.x * id, r.y * id), pack_bf16(r.z * id, r.w * id));
-  }
-};
-
-// Window mode: CTA c looks at the tiles that attention CTA c began or ended
-// with; the rows of a split one are shared out over the CTAs it was split over.
+// Window mode: CTA c looks at the tiles that share c of the wide list, and
+// shares 2c and 2c + 1 of the narrow one, began or ended with; the rows of a
+// split tile are shared out over the shares that it was split over.
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Work work, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x;
-  const uint4 seg[2] = {ld_dep(reinterpret_cast<const uint4*>(work.seg + 2 * c)),
-                        ld_dep(reinterpret_cast<const uint4*>(work.seg + 2 * c + 1))};
+  uint4 parts[6];
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const uint4 a = seg[side];
+  for (int x = 0; x < 6; ++x) {
+    const int slot = x < 2 ? 2 * blockIdx.x + x : 2 * kMaxCtas + 4 * blockIdx.x + x - 2;
+    parts[x] = ld_dep(reinterpret_cast<const uint4*>(work.parts + slot));
+  }
+#pragma unroll
+  for (int x = 0; x < 6; ++x) {
+    const uint4 a = parts[x];
     if (!a.w) continue;
+    const int share = x < 2 ? blockIdx.x : 2 * blockIdx.x + ((x - 2) >> 1), wide = x < 2;
     const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, rows = kGroup * static_cast<int>(a.y >> 8);
-    for (int r = c - lo + n * warp; r < rows; r += n * kMergeWarps) {
-      Fold f;
-      f.add(work, n, lane, [&](int i) {
-        return static_cast<int64_t>(i == 0 ? static_cast<int>(a.w) - 1 : 2 * (lo + i)) * work.rows_cap + r;
-      });
-      f.store(out, (static_cast<int64_t>(a.x) + (r >> 3)) * kNumQHeads + (a.y & 0xff) * kGroup + (r & 7), lane);
+    const int64_t slots = work.slots[wide];
+    const int cap = work.rows[wide];
+    auto at = [&](int i) -> int64_t {
+      return slots + static_cast<int64_t>(i == 0 ? static_cast<int>(a.w) - 1 : 2 * (lo + i)) * cap;
+    };
+    __nv_bfloat16* const to = out + (static_cast<int64_t>(a.x) * kNumQHeads + (a.y & 0xff) * kGroup) * kHeadDim;
+    if (n <= 4) {   // few partials: the 8 rows of a query at a time keep enough loads in flight
+      for (int q = share - lo + n * warp; q < rows / kGroup; q += n * kMergeWarps)
+        fold_query(work, n, lane, [&](int i) -> int64_t { return at(i) + q * kGroup; }, to + static_cast<int64_t>(q) * kNumQHeads * kHeadDim);
+    } else {
+      for (int r = share - lo + n * warp; r < rows; r += n * kMergeWarps)
+        fold_rows<1>(work, n, lane, [&](int i) -> int64_t { return at(i) + r; },
+                     to + (static_cast<int64_t>(r >> 3) * kNumQHeads + (r & 7)) * kHeadDim);
     }
   }
 }
@@ -1202,43 +1412,49 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Work 
   int ends[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) ends[i] = ld_dep(work.ends + i * static_cast<int64_t>(pairs) + pair);
-  if (!ok) return;
+  if (!ok || ends[2] == kNone) return;   // (kNone: the output is written)
+  auto many = [&](int first, int last) {
+    return first == kNone ? 0 : first & kEndWhole ? 1 : last - (first & kEndShare) + 1;
+  };
+  const int n0 = many(ends[0], ends[1]), n1 = many(ends[2], ends[3]);
   const int64_t row = static_cast<int64_t>(pair) * kGroup + h;   // query * 64 + head
-  Fold f;
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    const int first = ends[2 * part], last = ends[2 * part + 1];
-    if (first == kNone) continue;
-    const int c0 = first & 0xff;
-    const int64_t slots = 2ll * kNumQHeads * B + ((first >> kEndPlace) & 0xff) * kGroup + h;
-    const bool whole = first & kEndWhole;
-    f.add(work, whole ? 1 : last - c0 + 1, lane, [&](int i) {
-      return whole ? row + part * static_cast<int64_t>(kNumQHeads) * B
-                   : slots + (2ll * (c0 + i) + (i == 0 && (first & kEndSlot) ? 1 : 0)) * work.rows_cap;
-    });
-  }
-  f.store(out, row, lane);
+  fold_rows<1>(work, n0 + n1, lane,
+               [&](int i) -> int64_t {
+                 const bool own = i >= n0;
+                 const int first = own ? ends[2] : ends[0];
+                 if (own) i -= n0;
+                 if (first & kEndWhole) return row + (own ? static_cast<int64_t>(kNumQHeads) * B : 0);
+                 const int kind = first & kEndWide ? 1 : 0;
+                 return work.slots[kind] + (2ll * ((first & kEndShare) + i) + (i == 0 && (first & kEndSlot) ? 1 : 0)) * work.rows[kind] +
+                        ((first >> kEndPlace) & 31) * kGroup + h;
+               },
+               out + row * kHeadDim);
 }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-// Rows of a record: a tile's queries x 8 heads.
-int rows_cap(int queries) { return kGroup * (queries < kWideQ ? queries : kWideQ); }
-// The workspace's parts: rows and their log-sum-exps, the segments or the ends, the verdict.
-size_t layout(Work* w, void* at, int64_t place_rows, int queries, int64_t pairs) {
-  const int64_t rows = place_rows + 2ll * kMaxCtas * rows_cap(queries);
-  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4);
-  const size_t seg = 2 * kMaxCtas * sizeof(int4), ends = round16(4 * pairs * 4), ok = 16;
+// The workspace's parts: counts, rows and their log-sum-exps, parts, ends, the
+// verdict.  `queries`: the most queries of an entry; `pairs`: prefix mode's.
+size_t layout(Work* w, void* at, int64_t places, int queries, int64_t pairs) {
+  const int narrow = kGroup * (queries < kNarrowQ ? queries : kNarrowQ);
+  const int wide = queries <= kNarrowQ ? 0 : kGroup * (queries < kWideQ ? queries : kWideQ);
+  const int64_t rows = places + 2ll * kMaxCtas * wide + 4ll * kMaxCtas * narrow;
+  const size_t count = 4 * kMaxCtas * sizeof(int), parts = 6 * kMaxCtas * sizeof(int4);
+  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4), ends = round16(4 * pairs * 4), ok = 16;
   if (w) {
     char* p = static_cast<char*>(at);
-    w->o = reinterpret_cast<float*>(p);
+    w->count = reinterpret_cast<int*>(p);
+    w->o = reinterpret_cast<float*>(p += count);
     w->lse = reinterpret_cast<float*>(p += o);
-    w->seg = reinterpret_cast<int4*>(p += lse);
-    w->ends = reinterpret_cast<int*>(p += seg);
+    w->parts = reinterpret_cast<int4*>(p += lse);
+    w->ends = reinterpret_cast<int*>(p += parts);
     w->ok = reinterpret_cast<int*>(p += ends);
-    w->rows_cap = rows_cap(queries);
+    w->rows[0] = narrow;
+    w->rows[1] = wide;
+    w->slots[1] = places;
+    w->slots[0] = places + 2ll * kMaxCtas * wide;
   }
-  return o + lse + seg + ends + ok;
+  return count + o + lse + parts + ends + ok;
 }
 size_t window_layout(Work* w, void* at, int max_q) { return layout(w, at, 0, max_q, 0); }
 size_t prefix_layout(Work* w, void* at, int B) {
@@ -1246,7 +1462,7 @@ size_t prefix_layout(Work* w, void* at, int B) {
 }
 
 std::mutex g_mu;
-bool g_attr_set[64] = {};
+bool g_attr_set[3][64] = {};
 
 int encode_pool(CUtensorMap* map, const void* base, int64_t n_slots) {
   const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(n_slots) * kNumKVHeads * kChunkTokens};
@@ -1282,38 +1498,41 @@ int check(const void* q, const void* k_pool, const void* v_pool, int64_t n_slots
   return LSA_OK;
 }
 
+template <Mode kMode>
 int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool, const void* v_pool, float scale, void* out,
-           int64_t max_units, void* stream) {
+           int64_t most_units, void* stream) {
   const int sms = device_sm_count();
   if (sms <= 0 || !tensor_map_encoder()) return LSA_ERR_NO_DEVICE;
   int dev = 0;
   cudaGetDevice(&dev);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    if (dev < 64 && !g_attr_set[dev]) {
-      if (cudaFuncSetAttribute(pool_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
+    if (dev < 64 && !g_attr_set[kMode][dev]) {
+      if (cudaFuncSetAttribute(pool_attn_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
         cudaGetLastError();
         return LSA_ERR_CUDA;
       }
-      g_attr_set[dev] = true;
+      g_attr_set[kMode][dev] = true;
     }
   }
-  CUtensorMap tm_k, tm_v, tm_q, tm_q1;
+  CUtensorMap tm_k, tm_v, tm_q16, tm_q8, tm_q1;
   int st = encode_pool(&tm_k, k_pool, plan.n_slots);
   if (st == LSA_OK) st = encode_pool(&tm_v, v_pool, plan.n_slots);
-  if (st == LSA_OK) st = encode_q(&tm_q, q, plan.rows, kHalfQ);
+  if (st == LSA_OK) st = encode_q(&tm_q16, q, plan.rows, kWideQ / 2);
+  if (st == LSA_OK) st = encode_q(&tm_q8, q, plan.rows, kNarrowQ);
   if (st == LSA_OK) st = encode_q(&tm_q1, q, plan.rows, 1);
   if (st != LSA_OK) return st;
+  // As many CTAs as the most that there can be to do is worth, one per SM.
   const int most = sms < kMaxCtas ? sms : kMaxCtas;
-  const int64_t want = (max_units + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
+  const int64_t want = (most_units + kMinShare - 1) / kMinShare;
   const int grid = want < most ? static_cast<int>(want) : most;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-  launch_pdl(true, pool_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q, tm_q1, plan, work,
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(out);
+  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
-  if (plan.prefix_mode)
+  if (kMode == kPrefixes)
     launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(kMergeThreads), 0, s, work, plan.B, o);
-  else
+  else if (kMode == kWindow)
     launch_pdl(true, window_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, s, work, o);
   return launch_status();
 }
@@ -1355,8 +1574,11 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
   pool::window_layout(&work, workspace, max_q);
   // A bound of the units: every tile sees its window, its queries' span and the sinks.
   const int64_t seen = static_cast<int64_t>(plan.window) / kChunkTokens + 3 + plan.sinks / kChunkTokens + 1;
-  const int64_t units = kNumKVHeads * (T / pool::kWideQ + B) * (seen < max_chunks ? seen : max_chunks);
-  return pool::launch(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
+  const int64_t tiles = T / pool::kWideQ + B;
+  const int64_t units = kNumKVHeads * tiles * ((seen < max_chunks ? seen : max_chunks) + pool::kTileCost);
+  return max_q <= pool::kNarrowQ
+             ? pool::launch<pool::kWindowNarrow>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream)
+             : pool::launch<pool::kWindow>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
 }
 
 size_t lsa_prefix_attn_workspace_size(int B, int n_groups) {
@@ -1378,7 +1600,6 @@ int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool
   if (!workspace || workspace_bytes < pool::prefix_layout(nullptr, nullptr, B)) return LSA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LSA_ERR_MISALIGNED;
   pool::Plan plan = {};
-  plan.prefix_mode = 1;
   plan.B = B;
   plan.groups = n_groups;
   plan.rows = B;
@@ -1389,12 +1610,14 @@ int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool
   plan.group_table = prefix_table;
   plan.max_chunks = max_chunks;
   plan.group_chunks = max_prefix_chunks;
+  plan.max_q = B;
   plan.n_slots = n_slots;
   pool::Work work;
   pool::prefix_layout(&work, workspace, B);
   const int64_t tiles = n_groups > 0 ? B / pool::kWideQ + n_groups : 0;
-  const int64_t units = kNumKVHeads * (tiles * max_prefix_chunks + static_cast<int64_t>(B) * max_chunks);
-  return pool::launch(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
+  const int64_t units = kNumKVHeads * (tiles * (static_cast<int64_t>(max_prefix_chunks) + pool::kTileCost) +
+                                       static_cast<int64_t>(B) * (max_chunks + pool::kTileCost));
+  return pool::launch<pool::kPrefixes>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
 }
 
 }  // extern "C"

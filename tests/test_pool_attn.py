@@ -58,8 +58,8 @@ def test_prefix_refuses(L, bad, status):
 def test_workspace_sizes(L):
     w = L.lsa_window_attn_workspace_size
     assert w(0, 1) == w(4097, 1) == w(1, 0) == 0
-    # two records for each of 160 CTAs: rows of 128 floats and a log-sum-exp
-    assert 0 < w(1, 1) - 2 * 160 * 8 * 129 * 4 < 1 << 16
+    # two records for each of 160 CTAs' two shares: rows of 128 floats and a log-sum-exp
+    assert 0 < w(1, 1) - 4 * 160 * 8 * 129 * 4 < 1 << 16
     assert w(1, 32) == w(4096, 1 << 20) and w(1, 31) < w(1, 32)
     x = L.lsa_prefix_attn_workspace_size
     assert x(0, 0) == x(4097, 1) == x(1, 2) == x(1, -1) == 0
