@@ -103,12 +103,13 @@ enum Mode { kWindowNarrow, kWindow, kPrefixes };
 // share c has two records, slots 2c and 2c + 1, of as many rows as its kind of
 // tile has.  In prefix mode the rows of a whole tile have places of their own,
 // 64 per sequence for its prefix and 64 for its own tokens, since a sequence's
-// output joins both.
+// output joins both.  Place says how a query's rows lie there.
 struct Work {
-  float* o;          // [rows][128], normalised: the places, the wide slots, the narrow slots
+  float* o;          // 128 values a row, normalised: the places, the wide slots, the narrow slots
   float* lse;        // [rows], base 2
   int64_t slots[2];  // first row of the narrow slots, of the wide ones
-  int rows[2];       // rows of a narrow record, of a wide one
+  int rows[2];       // rows of a narrow slot, of a wide one
+  int block_rows[2]; // rows of one of its blocks
   int* count;        // kWindowNarrow: [2 kMaxCtas][2 warps], by a tile's first share: units that
                      // its partials hold so far, zero between calls
   int4* parts;       // kWindow: by slot (wide, then narrow), its tile: first query, KV head and
@@ -118,8 +119,8 @@ struct Work {
   int* ok;           // prefix mode: the offsets were valid
 };
 // The first partial of a (sequence, KV head): its share, slot 2c + bit, whether
-// of the wide list, the query's place in the tile, or that the rows are in
-// their own place; kNone: no partial.
+// of the wide list, the query's block and number there, or that the rows are
+// in their own place; kNone: no partial.
 constexpr int kEndShare = 0x3ff, kEndSlot = 1 << 10, kEndWide = 1 << 11, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
 
 // The queries and the keys of one list entry: a sequence, or a group over its prefix.
@@ -268,17 +269,21 @@ struct Cursor {
   }
   __device__ int row(bool wide) const { return s.q0 + (wide ? t * kWideQ : s.nq - s.nq % kWideQ); }
   // At place r of entry `entry`, whose KV heads have per_head places each; the
-  // place in the list is u.
-  __device__ void start(const Plan& p, bool wide, int entry, const List& l, int64_t per_head, int64_t r, int64_t u) {
+  // place in the list is u.  (The whole warp.)
+  __device__ void start(const Plan& p, bool wide, int entry, const List& l, int64_t per_head, int64_t r, int64_t u, int lane) {
     v = entry;
     s = l;
     tiles = tiles_of(s, wide);
     g = static_cast<int>(quotient(r, per_head));
     r -= g * per_head;
-    int lo = 0, hi = tiles - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (span<kPrefix>(p, s, wide, mid) <= r) lo = mid; else hi = mid - 1;
+    // The last tile that starts at or before r, 32 ways at a time.
+    int lo = 0, n = tiles;
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lo + lane * step;
+      const unsigned at_or_before = __ballot_sync(0xffffffffu, lane * step < n && span<kPrefix>(p, s, wide, i) <= r);
+      const int k = 31 - __clz(at_or_before);   // lane 0's is
+      n = min(step, n - k * step);
+      lo += k * step;
     }
     t = lo;
     r -= span<kPrefix>(p, s, wide, t);
@@ -525,26 +530,34 @@ __device__ __forceinline__ void fewer_registers() {
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the shares come out of the block's own registers");
 
-// Exclusive prefix sum of `x` over the block (kWarps warps) and the total.
-template <int kWarps>
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sm, int64_t* total) {
+// Exclusive prefix sums of x[0 .. kSums - 1] over the block (kWarps warps), and the totals.
+template <int kWarps, int kSums>
+__device__ __forceinline__ void block_scan(const int64_t* x, int64_t* before, int64_t* total, int64_t* sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t inc = x;
+  int64_t inc[kSums];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += y;
+  for (int k = 0; k < kSums; ++k) {
+    inc[k] = x[k];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc[k], off);
+      if (lane >= off) inc[k] += y;
+    }
+    if (lane == 31) sm[k * kWarps + warp] = inc[k];
   }
-  if (lane == 31) sm[warp] = inc;
   __syncthreads();
-  int64_t before = 0, sum = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm[w];
-    sum += sm[w];
+  for (int k = 0; k < kSums; ++k) {
+    int64_t sum = 0;
+    before[k] = inc[k] - x[k];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int64_t y = sm[k * kWarps + w];
+      if (w < warp) before[k] += y;
+      sum += y;
+    }
+    total[k] = sum;
   }
-  *total = sum;
-  return before + inc - x;
 }
 
 // ---- folding the partials -----------------------------------------------------
@@ -559,77 +572,83 @@ __device__ __forceinline__ float ld_l2(const float* p) {
   asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
-// The kRows rows from a first one on, of the n partials whose first rows are
-// row(0) .. row(n - 1): joins them in that order and writes bf16 to out.  A warp,
-// 4 dims a lane; the loads of 32 / kRows partials are in flight together.
-template <int kRows, typename Row>
-__device__ __forceinline__ void fold_rows(const Work& w, int n, int lane, Row row, __nv_bfloat16* out) {
-  constexpr int kBatch = kRows >= 8 ? 2 : 16 / kRows;
-  float m[kRows], den[kRows];
-  float4 acc[kRows];
+// Where the 8 rows (query heads of a KV head) of a query lie in a partial: dims 4 c
+// .. 4 c + 3 of row h at work.o + o + c * stride + 4 h, the log-sum-exp at work.lse
+// + lse + h.  A slot holds a block of up to 4 queries for each warp that writes
+// it, so that a warp, a thread per row, stores 16 bytes a thread side by side.
+struct Place {
+  int64_t o, lse;
+  int stride;
+};
+__device__ __forceinline__ Place slot_place(const Work& w, int wide, int slot, int block, int query) {
+  const int rows = w.block_rows[wide];
+  const int64_t first = w.slots[wide] + static_cast<int64_t>(slot) * w.rows[wide] + block * rows;
+  return {first * kHeadDim + query * (kGroup * 4), first + query * kGroup, rows * 4};
+}
+// Prefix mode, a whole tile's: of a sequence's prefix, or of its own tokens.
+__device__ __forceinline__ Place own_place(const Work& w, int B, int b, int g, bool own) {
+  const int64_t first = (static_cast<int64_t>(own ? B : 0) + b) * kNumQHeads + g * kGroup;
+  return {first * kHeadDim, first, kGroup * 4};
+}
+
+// The 8 rows of a query: joins its n partials at place(0) .. place(n - 1), in
+// that order, and writes the output.  A warp; lane i has row i % 8 and the dims
+// 4 c .. 4 c + 3 with c % 4 = i / 8.  The loads of 4 partials are in flight
+// together.
+template <typename At>
+__device__ __forceinline__ void fold_query(const Work& w, int n, int lane, At place, __nv_bfloat16* out) {
+  constexpr int kBatch = 4, kPieces = kHeadDim / 16;
+  const int h = lane & 7, c0 = lane >> 3;
+  float m = -INFINITY, den = 0.f;
+  float4 acc[kPieces];
 #pragma unroll
-  for (int h = 0; h < kRows; ++h) {
-    m[h] = -INFINITY;
-    den[h] = 0.f;
-    acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int k = 0; k < kPieces; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int i = 0; i < n; i += kBatch) {
-    float lse[kBatch][kRows];
-    uint4 a[kBatch][kRows];
+    float lse[kBatch];
+    uint4 a[kBatch][kPieces];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
+      lse[x] = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < kRows; ++h) {
-        lse[x][h] = -INFINITY;
-        a[x][h] = make_uint4(0, 0, 0, 0);
-      }
+      for (int k = 0; k < kPieces; ++k) a[x][k] = make_uint4(0, 0, 0, 0);
       if (i + x < n) {
-        const int64_t r = row(i + x);
+        const Place p = place(i + x);
+        lse[x] = ld_l2(w.lse + p.lse + h);
 #pragma unroll
-        for (int h = 0; h < kRows; ++h) {
-          lse[x][h] = ld_l2(w.lse + r + h);
-          a[x][h] = ld_l2(reinterpret_cast<const float4*>(w.o + (r + h) * kHeadDim) + lane);
-        }
+        for (int k = 0; k < kPieces; ++k)
+          a[x][k] = ld_l2(reinterpret_cast<const float4*>(w.o + p.o + h * 4 + (c0 + 4 * k) * p.stride));
       }
     }
+    float top = m;
 #pragma unroll
-    for (int h = 0; h < kRows; ++h) {
-      float top = m[h];
+    for (int x = 0; x < kBatch; ++x) top = max3(top, lse[x], lse[x]);   // (a row that is not a number stays so)
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = fast_exp2(m - ref);
+    m = top;
+    den *= f;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) top = max3(top, lse[x][h], lse[x][h]);   // (a row that is not a number stays so)
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float f = fast_exp2(m[h] - ref);
-      m[h] = top;
-      den[h] *= f;
-      acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
+    for (int k = 0; k < kPieces; ++k) {
+      acc[k].x *= f; acc[k].y *= f; acc[k].z *= f; acc[k].w *= f;
+    }
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const float wt = fast_exp2(lse[x][h] - ref);
-        den[h] += wt;
-        acc[h].x = fmaf(wt, __uint_as_float(a[x][h].x), acc[h].x);
-        acc[h].y = fmaf(wt, __uint_as_float(a[x][h].y), acc[h].y);
-        acc[h].z = fmaf(wt, __uint_as_float(a[x][h].z), acc[h].z);
-        acc[h].w = fmaf(wt, __uint_as_float(a[x][h].w), acc[h].w);
+    for (int x = 0; x < kBatch; ++x) {
+      const float wt = fast_exp2(lse[x] - ref);
+      den += wt;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        acc[k].x = fmaf(wt, __uint_as_float(a[x][k].x), acc[k].x);
+        acc[k].y = fmaf(wt, __uint_as_float(a[x][k].y), acc[k].y);
+        acc[k].z = fmaf(wt, __uint_as_float(a[x][k].z), acc[k].z);
+        acc[k].w = fmaf(wt, __uint_as_float(a[x][k].w), acc[k].w);
       }
     }
   }
+  const float id = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-  for (int h = 0; h < kRows; ++h) {
-    const float id = den[h] == 0.f ? 0.f : 1.f / den[h];
-    *reinterpret_cast<uint2*>(out + h * kHeadDim + 4 * lane) =
-        make_uint2(pack_bf16(acc[h].x * id, acc[h].y * id), pack_bf16(acc[h].z * id, acc[h].w * id));
-  }
-}
-template <typename Row>
-__device__ __forceinline__ void fold_query(const Work& w, int n, int lane, Row row, __nv_bfloat16* out) {
-  if (n <= 2) {
-    fold_rows<kGroup>(w, n, lane, row, out);
-  } else {
-#pragma unroll 1
-    for (int h = 0; h < kGroup; h += 4)
-      fold_rows<4>(w, n, lane, [&](int i) -> int64_t { return row(i) + h; }, out + h * kHeadDim);
-  }
+  for (int k = 0; k < kPieces; ++k)
+    *reinterpret_cast<uint2*>(out + h * kHeadDim + 4 * (c0 + 4 * k)) =
+        make_uint2(pack_bf16(acc[k].x * id, acc[k].y * id), pack_bf16(acc[k].z * id, acc[k].w * id));
 }
 
 // A segment: the units of one tile that a share has.  The planners write them to
@@ -770,10 +789,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   }
   bad = __syncthreads_or(bad);
   if (bad) mine[0] = mine[1] = 0;
-  int64_t total[2];
-  int64_t before[2] = {block_scan<kThreads / 32>(mine[0], scan, &total[0]), 0};
-  total[1] = 0;
-  if (kHasWide) before[1] = block_scan<kThreads / 32>(mine[1], scan + 16, &total[1]);
+  int64_t total[2] = {0, 0};
+  int64_t before[2];
+  block_scan<kThreads / 32, kHasWide ? 2 : 1>(mine, before, total, scan);
   const Partition part_n(total[0], 2 * gridDim.x), part_w(total[1], gridDim.x);
   if (part_n.base >= (1 << 30) || part_w.base >= (1 << 30)) bad = 1;   // a share counts its units in 32 bits
   if (sm & 1023u) {                      // the 128-byte swizzle repeats every 1024 bytes
@@ -839,7 +857,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         more = !bad && u < cur.end && u < all;
         if (more) {
           const Found& f = found[x];
-          cur.start(plan, x == 0, f.v, f.s, f.per_head, f.r, u);
+          cur.start(plan, x == 0, f.v, f.s, f.per_head, f.r, u, lane);
           more = cur.units() > 0;
         }
       };
@@ -887,23 +905,32 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             s->table = cur.s.table;
             s->ident = cur.s.ident;
           }
-          if (!kPrefix && !(begins && ends)) {
+          if (kFold && !(begins && ends)) {
             const int lo = begins ? share : part.share_of(cur.at + kTileCost);
             const int hi = ends ? share : part.share_of(cur.at + kTileCost + cur.n - 1);
-            const int slot0 = 2 * lo + (part.start(lo) >= cur.at ? 0 : 1);   // there it may come after other tiles
             if (lane == 0) {
-              if (kMode == kWindow)
-                work.parts[(x == 0 ? 0 : 2 * kMaxCtas) + 2 * share + (put ? 1 : 0)] =
-                    make_int4(cur.row(wide), cur.g | (cur.cnt << 8), lo | (hi << 16), slot0 + 1);
               s->lo = lo;
               s->hi = hi;
-              s->slot0 = slot0;
+              s->slot0 = 2 * lo + (part.start(lo) >= cur.at ? 0 : 1);   // there it may come after other tiles
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(sm + kSegFull + 8 * place);
+        if (more) {
+          const bool wide = x == 0;
+          if (kMode == kWindow) {   // what the merge has to know
+            const bool begins = cur.j == 0, ends = cur.j + cur.units() == cur.n;
+            if (!(begins && ends)) {
+              const int lo = begins ? share : part.share_of(cur.at + kTileCost);
+              const int hi = ends ? share : part.share_of(cur.at + kTileCost + cur.n - 1);
+              if (lane == 0)
+                work.parts[(wide ? 0 : 2 * kMaxCtas) + 2 * share + (put ? 1 : 0)] =
+                    make_int4(cur.row(wide), cur.g | (cur.cnt << 8), lo | (hi << 16), 2 * lo + (part.start(lo) >= cur.at ? 0 : 1) + 1);
             }
           }
           more = cur.next(plan, wide);
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(sm + kSegFull + 8 * place);
         ++put;
         return true;
       };
@@ -1251,83 +1278,77 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         tcgen05_fence_after();
         if (queries > 0) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          // Where the rows go: 128 bytes of a row per 8 lanes.  A thread holds a
-          // row, so the rows turn in the warp's 4 KiB of shared memory, 16-byte
-          // piece x of row y at place x ^ (y % 8) (no bank conflicts either way).
           const bool whole = sg.flags & kSegWhole, final = whole && (!kPrefix || (sg.flags & kSegAlone));
-          const int row0 = sg.row + i_first, head = sg.head;
-          // Output rows: (query, head); a record's: the same, a tile at a time.
-          const int64_t out_row = static_cast<int64_t>(row0) * kNumQHeads + head;
-          const int64_t places = static_cast<int64_t>(kNumQHeads) * plan.B;
-          int64_t rec = out_row;
-          int q_rows = kNumQHeads;                   // rows from a query to the next
-          if (whole) {
-            if (!(sg.flags & kSegGroup)) rec += places;   // (prefix mode; a window's whole tile is final)
-          } else {
-            rec = work.slots[wide] + (2ll * sg.share + (sg.index > 0)) * work.rows[wide] + i_first * kGroup;
-            q_rows = kGroup;
-          }
-          uint8_t* const mine = smem + kTurnAt + warp * kTurnBytes;
-          uint8_t* const row_at = mine + lane * 128;
-          // fp32 records go 32 columns at a time, bf16 outputs 64.
-          uint8_t* to = final ? reinterpret_cast<uint8_t*>(out + out_row * kHeadDim)
-                              : reinterpret_cast<uint8_t*>(work.o + rec * kHeadDim);
-          const int row_bytes = final ? 2 * kHeadDim : 4 * kHeadDim;
+          const int row0 = sg.row + i_first, head = sg.head;   // the warp's first query, its first query head
+          if (final) {
+            // Output rows (query, head), 128 bytes of a row per 8 lanes.  A thread
+            // holds a row, so the rows turn in the warp's 4 KiB of shared memory,
+            // 16-byte piece x of row y at place x ^ (y % 8) (no bank conflicts
+            // either way).
+            uint8_t* const mine = smem + kTurnAt + warp * kTurnBytes;
+            uint8_t* const row_at = mine + lane * 128;
+            const uint8_t* const from = mine + (lane >> 3) * 128;
+            uint8_t* to = reinterpret_cast<uint8_t*>(
+                out + ((static_cast<int64_t>(row0) * kNumQHeads + head + (lane >> 3)) * kHeadDim + (lane & 7) * 8));
 #pragma unroll 1
-          for (int c = 0; c < kHeadDim; c += 32) {
-            float o[32];
-            tmem_ld32(o_col0 + c, o);
-            tmem_wait_ld(o, 32);
+            for (int c = 0; c < kHeadDim; c += 64, to += 128) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= inv;
-            if (final) {
-              const int z = (c >> 3) & 4;
+              for (int z = 0; z < 8; z += 4) {
+                float o[32];
+                tmem_ld32(o_col0 + c + 8 * z, o);
+                tmem_wait_ld(o, 32);
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                               pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-              if (!z) continue;
-            } else {
+                for (int x = 0; x < 32; ++x) o[x] *= inv;
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                *reinterpret_cast<float4*>(row_at + ((x ^ (lane & 7)) << 4)) =
-                    make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                for (int x = 0; x < 4; ++x)
+                  *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
+                      make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                                 pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
+              }
+              __syncwarp();
+#pragma unroll
+              for (int x = 0; x < 8; ++x)            // rows 4 x + lane / 8: query x / 2
+                if ((x >> 1) < queries)
+                  *reinterpret_cast<uint4*>(to + (x >> 1) * (kNumQHeads * kHeadDim * 2) + (x & 1) * (4 * kHeadDim * 2)) =
+                      *reinterpret_cast<const uint4*>(from + x * 512 + (((lane & 7) ^ (4 * (x & 1) + (lane >> 3))) << 4));
+              __syncwarp();
             }
-            __syncwarp();
+          } else {
+            const Place at_o = whole ? own_place(work, plan.B, row0 + (lane >> 3), head >> 3, !(sg.flags & kSegGroup))
+                                     : slot_place(work, wide, 2 * sg.share + (sg.index > 0), wide ? warp : wq, lane >> 3);
+            float* const to = work.o + at_o.o + (lane & 7) * 4;
+            const bool valid = (lane >> 3) < queries;
+#pragma unroll 1
+            for (int c = 0; c < kHeadDim; c += 32) {
+              float o[32];
+              tmem_ld32(o_col0 + c, o);
+              tmem_wait_ld(o, 32);
+              if (valid) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const int y = 4 * x + (lane >> 3);     // row of the warp: query y / 8, head y % 8
-              if ((y >> 3) < queries)
-                *reinterpret_cast<uint4*>(to + ((y >> 3) * q_rows + (y & 7)) * row_bytes + (lane & 7) * 16) =
-                    *reinterpret_cast<const uint4*>(mine + y * 128 + (((lane & 7) ^ (y & 7)) << 4));
+                for (int x = 0; x < 8; ++x)
+                  *reinterpret_cast<float4*>(to + (c / 4 + x) * at_o.stride) =
+                      make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+              }
             }
-            __syncwarp();
-            to += 128;
+            if (valid) work.lse[at_o.lse + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
           }
           tcgen05_fence_before();
-          if (!final) {
-            if ((lane >> 3) < queries)
-              work.lse[rec + (lane >> 3) * q_rows + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
-            if (kFold) {
-              // Few queries a sequence: the warp that adds a tile's last units
-              // folds its rows (the other shares' are from the same warp there).
-              int* const count = work.count + sg.lo * 2 + wq;
-              int before = 0;
+          if (kFold && !final) {
+            // Few queries a sequence: the warp that adds a tile's last units folds
+            // its rows (the other shares' are from the same warp there).
+            int* const count = work.count + sg.lo * 2 + wq;
+            int before = 0;
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) before = atomicAdd(count, n);
+            if (__shfl_sync(0xffffffffu, before, 0) + n == sg.all) {
+              if (lane == 0) *count = 0;
               __threadfence();
-              __syncwarp();
-              if (lane == 0) before = atomicAdd(count, n);
-              if (__shfl_sync(0xffffffffu, before, 0) + n == sg.all) {
-                if (lane == 0) *count = 0;
-                __threadfence();
-                const int lo = sg.lo, slot0 = sg.slot0, rows = work.rows[0];
-                for (int i = 0; i < queries; ++i) {
-                  const int64_t at0 = work.slots[0] + (i_first + i) * kGroup;
-                  fold_query(work, sg.hi - lo + 1, lane,
-                             [&](int x) -> int64_t { return at0 + static_cast<int64_t>(x == 0 ? slot0 : 2 * (lo + x)) * rows; },
-                             out + (out_row + static_cast<int64_t>(i) * kNumQHeads) * kHeadDim);
-                }
-              }
+              const int lo = sg.lo, slot0 = sg.slot0;
+              for (int i = 0; i < queries; ++i)
+                fold_query(work, sg.hi - lo + 1, lane,
+                           [&](int x) { return slot_place(work, 0, x == 0 ? slot0 : 2 * (lo + x), wq, i); },
+                           out + (static_cast<int64_t>(row0 + i) * kNumQHeads + head) * kHeadDim);
             }
           }
           if (kPrefix && lane < queries) {   // where the merge finds the partials
@@ -1336,7 +1357,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (j0 == 0)
               ends[part * pairs] = final ? kNone
                                          : sg.share | (sg.index > 0 ? kEndSlot : 0) | (wide ? kEndWide : 0) |
-                                               ((i_first + lane) << kEndPlace) | (whole ? kEndWhole : 0);
+                                               (((wide ? warp : wq) * 4 + lane) << kEndPlace) | (whole ? kEndWhole : 0);
             if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.share;
             if (sg.flags & kSegAlone) ends[0] = kNone;
           }
@@ -1364,6 +1385,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // ---- the merge kernels --------------------------------------------------------
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kPrefixMergeThreads = 64;
 
 // Window mode: CTA c looks at the tiles that share c of the wide list, and
 // shares 2c and 2c + 1 of the narrow one, began or ended with; the rows of a
@@ -1383,31 +1405,24 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Work 
     const uint4 a = parts[x];
     if (!a.w) continue;
     const int share = x < 2 ? blockIdx.x : 2 * blockIdx.x + ((x - 2) >> 1), wide = x < 2;
-    const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, rows = kGroup * static_cast<int>(a.y >> 8);
-    const int64_t slots = work.slots[wide];
-    const int cap = work.rows[wide];
-    auto at = [&](int i) -> int64_t {
-      return slots + static_cast<int64_t>(i == 0 ? static_cast<int>(a.w) - 1 : 2 * (lo + i)) * cap;
-    };
-    __nv_bfloat16* const to = out + (static_cast<int64_t>(a.x) * kNumQHeads + (a.y & 0xff) * kGroup) * kHeadDim;
-    if (n <= 4) {   // few partials: the 8 rows of a query at a time keep enough loads in flight
-      for (int q = share - lo + n * warp; q < rows / kGroup; q += n * kMergeWarps)
-        fold_query(work, n, lane, [&](int i) -> int64_t { return at(i) + q * kGroup; }, to + static_cast<int64_t>(q) * kNumQHeads * kHeadDim);
-    } else {
-      for (int r = share - lo + n * warp; r < rows; r += n * kMergeWarps)
-        fold_rows<1>(work, n, lane, [&](int i) -> int64_t { return at(i) + r; },
-                     to + (static_cast<int64_t>(r >> 3) * kNumQHeads + (r & 7)) * kHeadDim);
+    const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.y >> 8);
+    const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
+    for (int q = share - lo + n * warp; q < cnt; q += n * kMergeWarps) {
+      const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
+      fold_query(work, n, lane,
+                 [&](int k) { return slot_place(work, wide, k == 0 ? static_cast<int>(a.w) - 1 : 2 * (lo + k), block, i & 3); },
+                 out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + (a.y & 0xff) * kGroup) * kHeadDim);
     }
   }
 }
 
-// Prefix mode: a CTA per (sequence, KV head), a warp per query head: the
-// partials of its group's tile, then those of its own tokens.
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
+// Prefix mode: a warp per (sequence, KV head): the partials of its group's tile,
+// then those of its own tokens.
+__global__ void __launch_bounds__(kPrefixMergeThreads) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
-  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x, pairs = B * kNumKVHeads;   // (sequence, KV head)
+  const int lane = threadIdx.x & 31;
+  const int pairs = B * kNumKVHeads, pair = blockIdx.x * (kPrefixMergeThreads / 32) + (threadIdx.x >> 5);
   const int ok = ld_dep(work.ok);
   int ends[4];
 #pragma unroll
@@ -1417,18 +1432,17 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Work 
     return first == kNone ? 0 : first & kEndWhole ? 1 : last - (first & kEndShare) + 1;
   };
   const int n0 = many(ends[0], ends[1]), n1 = many(ends[2], ends[3]);
-  const int64_t row = static_cast<int64_t>(pair) * kGroup + h;   // query * 64 + head
-  fold_rows<1>(work, n0 + n1, lane,
-               [&](int i) -> int64_t {
-                 const bool own = i >= n0;
-                 const int first = own ? ends[2] : ends[0];
-                 if (own) i -= n0;
-                 if (first & kEndWhole) return row + (own ? static_cast<int64_t>(kNumQHeads) * B : 0);
-                 const int kind = first & kEndWide ? 1 : 0;
-                 return work.slots[kind] + (2ll * ((first & kEndShare) + i) + (i == 0 && (first & kEndSlot) ? 1 : 0)) * work.rows[kind] +
-                        ((first >> kEndPlace) & 31) * kGroup + h;
-               },
-               out + row * kHeadDim);
+  fold_query(work, n0 + n1, lane,
+             [&](int i) {
+               const bool own = i >= n0;
+               const int first = own ? ends[2] : ends[0];
+               if (own) i -= n0;
+               if (first & kEndWhole) return own_place(work, B, pair / kNumKVHeads, pair % kNumKVHeads, own);
+               return slot_place(work, first & kEndWide ? 1 : 0,
+                                 2 * ((first & kEndShare) + i) + (i == 0 && (first & kEndSlot) ? 1 : 0),
+                                 (first >> (kEndPlace + 2)) & 7, (first >> kEndPlace) & 3);
+             },
+             out + static_cast<int64_t>(pair) * kGroup * kHeadDim);
 }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
@@ -1436,8 +1450,8 @@ size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 // The workspace's parts: counts, rows and their log-sum-exps, parts, ends, the
 // verdict.  `queries`: the most queries of an entry; `pairs`: prefix mode's.
 size_t layout(Work* w, void* at, int64_t places, int queries, int64_t pairs) {
-  const int narrow = kGroup * (queries < kNarrowQ ? queries : kNarrowQ);
-  const int wide = queries <= kNarrowQ ? 0 : kGroup * (queries < kWideQ ? queries : kWideQ);
+  const int narrow = kGroup * (queries <= 4 ? queries : kNarrowQ);   // whole blocks of 4 queries, or one smaller block
+  const int wide = queries <= kNarrowQ ? 0 : kGroup * kWideQ;
   const int64_t rows = places + 2ll * kMaxCtas * wide + 4ll * kMaxCtas * narrow;
   const size_t count = 4 * kMaxCtas * sizeof(int), parts = 6 * kMaxCtas * sizeof(int4);
   const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4), ends = round16(4 * pairs * 4), ok = 16;
@@ -1451,6 +1465,8 @@ size_t layout(Work* w, void* at, int64_t places, int queries, int64_t pairs) {
     w->ok = reinterpret_cast<int*>(p += ends);
     w->rows[0] = narrow;
     w->rows[1] = wide;
+    w->block_rows[0] = narrow < 4 * kGroup ? narrow : 4 * kGroup;
+    w->block_rows[1] = 4 * kGroup;
     w->slots[1] = places;
     w->slots[0] = places + 2ll * kMaxCtas * wide;
   }
@@ -1531,7 +1547,8 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
-    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(kMergeThreads), 0, s, work, plan.B, o);
+    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads * 32 / kPrefixMergeThreads),
+               dim3(kPrefixMergeThreads), 0, s, work, plan.B, o);
   else if (kMode == kWindow)
     launch_pdl(true, window_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, s, work, o);
   return launch_status();
