@@ -666,8 +666,8 @@ int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const 
  * the other queries of the same 32 (a prompt's) that do not.
  * The work is cut into equal shares whatever the batch, and the partials of a
  * query are joined in a fixed order: repeated calls are bit-identical.  One
- * kernel, a programmatic dependent of its predecessor.  Device errors:
- * CAPACITY (cu_q not starting at 0, decreasing, past T, or an nq above max_q:
+ * kernel (max_q <= 8) or two, programmatic dependents of their predecessor.
+ * Device errors: CAPACITY (cu_q not starting at 0, decreasing, past T, or an nq above max_q:
  * nothing is computed), BAD_COUNT (seq_len outside [0, 64 max_chunks]: that
  * sequence's rows are zeros), BAD_SLOT (that chunk is read as zeros), TIMEOUT.
  */
@@ -702,13 +702,11 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
  *                chunk 0, whatever the prefix's length); suffix_len device
  *                int32 [B]
  *   workspace    device, >= lsa_prefix_attn_workspace_size(B, n_groups) bytes,
- *                16-byte aligned, zero before the first call (and again after a
- *                call that reported TIMEOUT): every call leaves the counts in it
- *                zero.  Calls that may overlap on the GPU need workspaces of
- *                their own, and a workspace serves one B (its layout)
+ *                16-byte aligned, no initialisation; calls that may overlap on
+ *                the GPU need workspaces of their own
  * Rows of a chunk past a length may hold anything.  Repeated calls are
- * bit-identical.  One kernel, a programmatic dependent of its predecessor.
- * Device errors: CAPACITY (cu_group not starting at 0, decreasing or past B: nothing is
+ * bit-identical.  Two kernels, both programmatic dependents of their
+ * predecessor.  Device errors: CAPACITY (cu_group not starting at 0, decreasing or past B: nothing is
  * computed), BAD_COUNT (a length out of range: that prefix, or that
  * sequence's own tokens, count as none), BAD_SLOT (that chunk is read as
  * zeros), TIMEOUT.

@@ -549,6 +549,26 @@ def lsa_sparse_decode_attn_noalloc(q, k_buf, v_buf, cu_kept, out, softmax_scale=
 
 ROPE_INTERLEAVED = 1
 
+# The calls below run once per layer and step, where a call's own time counts:
+# each looks its arguments over in one expression, and only when that fails do the
+# functions that say what is wrong with them run.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, device: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
+def _fits(t, dtype, device: int) -> bool:
+    """A contiguous tensor of the type on the current device."""
+    return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
 
 def _here(*tensors):
     """The tensors that are given live on the current device, whose stream the call uses."""
@@ -566,13 +586,26 @@ def _pool(t: torch.Tensor, name: str) -> int:
     return int(t.shape[0])
 
 
-def _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight):
-    """Checks of the arguments both forms share; the number of tokens."""
+_QKV_WIDTH = (NUM_Q_HEADS + 2 * NUM_KV_HEADS) * HEAD_DIM
+_POOL_ROWS = (NUM_KV_HEADS, CHUNK_TOKENS, HEAD_DIM)
+
+
+def _rope_fits(qkv, positions, inv_freq, q_out, q_weight, k_weight, dev: int) -> bool:
+    T = qkv.shape[0]
+    return (qkv.dtype is torch.bfloat16 and qkv.get_device() == dev and qkv.dim() == 2 and qkv.shape[1] == _QKV_WIDTH
+            and qkv.stride(1) == 1 and _fits(q_out, torch.bfloat16, dev) and q_out.shape == (T, NUM_Q_HEADS, HEAD_DIM)
+            and (inv_freq is None or (_fits(inv_freq, torch.float32, dev) and inv_freq.dim() == 1
+                                      and _fits(positions, torch.int32, dev) and positions.numel() == T))
+            and (q_weight is None or (_fits(q_weight, torch.float32, dev) and q_weight.numel() == HEAD_DIM))
+            and (k_weight is None or (_fits(k_weight, torch.float32, dev) and k_weight.numel() == HEAD_DIM)))
+
+
+def _rope_explain(qkv, positions, inv_freq, q_out, q_weight, k_weight):
+    """Raises for the argument that _rope_fits found wanting."""
     if not isinstance(qkv, torch.Tensor) or qkv.dtype != torch.bfloat16 or not qkv.is_cuda:
         raise TypeError("qkv must be a CUDA bfloat16 tensor")
-    width = (NUM_Q_HEADS + 2 * NUM_KV_HEADS) * HEAD_DIM
-    if qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
-        raise ValueError(f"qkv must be [T, {width}] with contiguous rows")
+    if qkv.dim() != 2 or qkv.shape[1] != _QKV_WIDTH or qkv.stride(1) != 1:
+        raise ValueError(f"qkv must be [T, {_QKV_WIDTH}] with contiguous rows")
     T = qkv.shape[0]
     _need(q_out, "q_out", torch.bfloat16)
     if tuple(q_out.shape) != (T, NUM_Q_HEADS, HEAD_DIM):
@@ -588,12 +621,23 @@ def _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight):
             if w.numel() != HEAD_DIM:
                 raise ValueError(f"{n} must have 128 values")
     _here(qkv, positions, inv_freq, q_out, q_weight, k_weight)
-    return T
+
+
+def _is(check, *args) -> bool:
+    """check(*args); an argument that is no tensor does not pass."""
+    try:
+        return check(*args)
+    except AttributeError:
+        return False
 
 
 def _row_stride(qkv) -> int:
     """Elements between rows; torch leaves the stride of a single row open."""
-    return qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
+    return qkv.stride(0) if qkv.shape[0] > 1 else _QKV_WIDTH
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def lsa_qk_norm_rope(qkv, positions, inv_freq, q_out, k_out, v_out=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -604,28 +648,37 @@ def lsa_qk_norm_rope(qkv, positions, inv_freq, q_out, k_out, v_out=None, q_weigh
     Rotates the first 2 * inv_freq.numel() dims of each query and key head by positions * inv_freq
     (rope_frequencies makes the table; None: no rotation), after the RMS norm with q_weight / k_weight fp32 [128]
     (None: no norm).  v_out None: the value heads are not copied."""
-    T = _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight)
+    dev = _current_device()
+    if not _is(_rope_fits, qkv, positions, inv_freq, q_out, q_weight, k_weight, dev):
+        _rope_explain(qkv, positions, inv_freq, q_out, q_weight, k_weight)
+    T = qkv.shape[0]
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None or n == "k_out":
+        if n == "v_out" and t is None:
+            continue
+        if not _is(_fits, t, torch.bfloat16, dev) or t.shape != (T, NUM_KV_HEADS, HEAD_DIM):
             _need(t, n, torch.bfloat16)
-            if tuple(t.shape) != (T, NUM_KV_HEADS, HEAD_DIM):
-                raise ValueError(f"{n} must be [T, 8, 128]")
-    _here(k_out, v_out)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _check("lsa_qk_norm_rope", _load().lsa_qk_norm_rope(
-        _ptr(qkv), _row_stride(qkv), T, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot,
-        float(rope_scale), ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), _ptr(k_out), _ptr(v_out),
-        _stream(stream)))
+            _here(t)
+            raise ValueError(f"{n} must be [T, 8, 128]")
+    st = (_lib or _load()).lsa_qk_norm_rope(
+        qkv.data_ptr(), _row_stride(qkv), T, _at(q_weight), _at(k_weight), eps, _at(positions), _at(inv_freq),
+        0 if inv_freq is None else 2 * inv_freq.numel(), rope_scale, ROPE_INTERLEAVED if interleaved else 0,
+        q_out.data_ptr(), k_out.data_ptr(), _at(v_out), _stream_of(stream, dev))
+    if st:
+        raise LsaError("lsa_qk_norm_rope", st)
 
 
-def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks,
-                          q_weight=None, k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
-    """lsa_qk_norm_rope with token t's K and V written to position cache_pos[t] of sequence seq_ids[t] in the
-    pools [slots, 8, 64, 128] (chunk_table [B, max_chunks], or None for the identity layout; cache_pos < 0: not
-    written)."""
-    T = _rope_args(qkv, positions, inv_freq, q_out, q_weight, k_weight)
-    n_slots = _pool(k_pool, "k_pool")
-    if _pool(v_pool, "v_pool") != n_slots:
+def _rope_pool_fits(T, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks, dev: int) -> bool:
+    return (_fits(k_pool, torch.bfloat16, dev) and _fits(v_pool, torch.bfloat16, dev) and k_pool.dim() == 4
+            and k_pool.shape[1:] == _POOL_ROWS and v_pool.shape == k_pool.shape
+            and _fits(seq_ids, torch.int32, dev) and seq_ids.numel() == T
+            and _fits(cache_pos, torch.int32, dev) and cache_pos.numel() == T
+            and (max_chunks > 0 if chunk_table is None else
+                 _fits(chunk_table, torch.int32, dev) and chunk_table.dim() == 2 and chunk_table.shape[1] == max_chunks))
+
+
+def _rope_pool_explain(T, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks):
+    """Raises for the argument that _rope_pool_fits found wanting."""
+    if _pool(v_pool, "v_pool") != _pool(k_pool, "k_pool"):
         raise ValueError("k_pool and v_pool must have the same shape")
     for t, n in ((seq_ids, "seq_ids"), (cache_pos, "cache_pos")):
         _need(t, n, torch.int32)
@@ -637,13 +690,29 @@ def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk
             raise ValueError("chunk_table must be [B, max_chunks]")
     elif max_chunks <= 0:
         raise ValueError("max_chunks must be positive")
-    B = chunk_table.shape[0] if chunk_table is not None else max(1, n_slots // int(max_chunks))
     _here(k_pool, v_pool, chunk_table, seq_ids, cache_pos)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _check("lsa_qk_norm_rope_pool", _load().lsa_qk_norm_rope_pool(
-        _ptr(qkv), _row_stride(qkv), T, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), rot,
-        float(rope_scale), ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), _ptr(k_pool), _ptr(v_pool), n_slots,
-        _ptr(chunk_table), _ptr(seq_ids), _ptr(cache_pos), B, int(max_chunks), _stream(stream)))
+
+
+def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks,
+                          q_weight=None, k_weight=None, eps=1e-6, interleaved=False, rope_scale=1.0, stream=None):
+    """lsa_qk_norm_rope with token t's K and V written to position cache_pos[t] of sequence seq_ids[t] in the
+    pools [slots, 8, 64, 128] (chunk_table [B, max_chunks], or None for the identity layout; cache_pos < 0: not
+    written)."""
+    dev = _current_device()
+    if not _is(_rope_fits, qkv, positions, inv_freq, q_out, q_weight, k_weight, dev):
+        _rope_explain(qkv, positions, inv_freq, q_out, q_weight, k_weight)
+    T = qkv.shape[0]
+    if not _is(_rope_pool_fits, T, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks, dev):
+        _rope_pool_explain(T, k_pool, v_pool, chunk_table, seq_ids, cache_pos, max_chunks)
+    n_slots = k_pool.shape[0]
+    B = chunk_table.shape[0] if chunk_table is not None else max(1, n_slots // max_chunks)
+    st = (_lib or _load()).lsa_qk_norm_rope_pool(
+        qkv.data_ptr(), _row_stride(qkv), T, _at(q_weight), _at(k_weight), eps, _at(positions), _at(inv_freq),
+        0 if inv_freq is None else 2 * inv_freq.numel(), rope_scale, ROPE_INTERLEAVED if interleaved else 0,
+        q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), n_slots, _at(chunk_table), seq_ids.data_ptr(),
+        cache_pos.data_ptr(), B, max_chunks, _stream_of(stream, dev))
+    if st:
+        raise LsaError("lsa_qk_norm_rope_pool", st)
 
 
 def new_window_attn_workspace(B: int, max_q: int, device=None) -> torch.Tensor:
@@ -655,28 +724,39 @@ def new_window_attn_workspace(B: int, max_q: int, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _pool_attn_args(q, k_pool, v_pool, chunk_table, lengths, max_chunks, out, workspace, name):
-    """Checks of the arguments both pool attentions share; slots, sequences and chunks per table row."""
+def _pool_attn_fits(q, k_pool, v_pool, chunk_table, lengths, max_chunks, out, workspace, dev: int) -> bool:
+    return (_fits(q, torch.bfloat16, dev) and q.dim() == 3 and q.shape[1:] == (NUM_Q_HEADS, HEAD_DIM)
+            and _fits(out, torch.bfloat16, dev) and out.shape == q.shape
+            and _fits(k_pool, torch.bfloat16, dev) and _fits(v_pool, torch.bfloat16, dev) and k_pool.dim() == 4
+            and k_pool.shape[1:] == _POOL_ROWS and v_pool.shape == k_pool.shape
+            and _fits(workspace, torch.uint8, dev) and _fits(lengths, torch.int32, dev)
+            and (max_chunks is not None if chunk_table is None else
+                 _fits(chunk_table, torch.int32, dev) and chunk_table.dim() == 2
+                 and chunk_table.shape[0] == lengths.numel()
+                 and (max_chunks is None or chunk_table.shape[1] == max_chunks)))
+
+
+def _pool_attn_explain(q, k_pool, v_pool, chunk_table, lengths, max_chunks, out, workspace, name):
+    """Raises for the argument that _pool_attn_fits found wanting."""
     _need(q, "q", torch.bfloat16)
     _need(out, "out", torch.bfloat16)
     _need(workspace, "workspace", torch.uint8)
     _need(lengths, name, torch.int32)
     if q.dim() != 3 or tuple(q.shape[1:]) != (NUM_Q_HEADS, HEAD_DIM) or out.shape != q.shape:
         raise ValueError("q and out must be [rows, 64, 128]")
-    n_slots = _pool(k_pool, "k_pool")
-    if _pool(v_pool, "v_pool") != n_slots:
+    if _pool(v_pool, "v_pool") != _pool(k_pool, "k_pool"):
         raise ValueError("k_pool and v_pool must have the same shape")
-    B = lengths.numel()
     if chunk_table is not None:
         _need(chunk_table, "chunk_table", torch.int32)
-        if chunk_table.dim() != 2 or chunk_table.shape[0] != B or (max_chunks is not None
-                                                                   and chunk_table.shape[1] != max_chunks):
+        if chunk_table.dim() != 2 or chunk_table.shape[0] != lengths.numel() or (max_chunks is not None
+                                                                                 and chunk_table.shape[1] != max_chunks):
             raise ValueError("chunk_table must be [B, max_chunks]")
-        max_chunks = chunk_table.shape[1]
     elif max_chunks is None:
         raise ValueError("the identity layout (no chunk_table) needs max_chunks")
     _here(q, k_pool, v_pool, chunk_table, lengths, out, workspace)
-    return n_slots, B, int(max_chunks)
+
+
+_ATTN_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 
 def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, max_q, window, n_sink, out, workspace,
@@ -686,25 +766,35 @@ def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, m
     Sequence b's queries are rows cu_q[b] .. cu_q[b+1]-1 of q [T, 64, 128] and the last of its seq_len[b] cached
     tokens, which the pools [slots, 8, 64, 128] hold by chunk_table [B, max_chunks] (None: identity layout); at
     most ``max_q`` per sequence.  out is bf16 like q; workspace from new_window_attn_workspace(B, max_q)."""
-    n_slots, B, max_chunks = _pool_attn_args(q, k_pool, v_pool, chunk_table, seq_len, int(max_chunks), out, workspace,
-                                             "seq_len")
-    _need(cu_q, "cu_q", torch.int32)
-    if cu_q.numel() != B + 1:
+    dev = _current_device()
+    if not _is(_pool_attn_fits, q, k_pool, v_pool, chunk_table, seq_len, max_chunks, out, workspace, dev):
+        _pool_attn_explain(q, k_pool, v_pool, chunk_table, seq_len, max_chunks, out, workspace, "seq_len")
+    B = seq_len.numel()
+    if not _is(_fits, cu_q, torch.int32, dev) or cu_q.numel() != B + 1:
+        _need(cu_q, "cu_q", torch.int32)
+        _here(cu_q)
         raise ValueError("cu_q must be [B + 1]")
-    _here(cu_q)
-    scale = 1.0 / math.sqrt(HEAD_DIM) if softmax_scale is None else float(softmax_scale)
-    _check("lsa_window_attn", _load().lsa_window_attn(
-        _ptr(q), q.shape[0], _ptr(k_pool), _ptr(v_pool), n_slots, _ptr(chunk_table), _ptr(cu_q), _ptr(seq_len), B,
-        max_chunks, int(max_q), int(window), int(n_sink), scale, _ptr(out), _ptr(workspace), workspace.numel(),
-        _stream(stream)))
+    st = (_lib or _load()).lsa_window_attn(
+        q.data_ptr(), q.shape[0], k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], _at(chunk_table),
+        cu_q.data_ptr(), seq_len.data_ptr(), B, max_chunks, max_q, window, n_sink,
+        _ATTN_SCALE if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream_of(stream, dev))
+    if st:
+        raise LsaError("lsa_window_attn", st)
 
 
 def new_prefix_attn_workspace(B: int, n_groups: int, device=None) -> torch.Tensor:
-    """A workspace for lsa_prefix_decode_attn, zeroed (every call leaves its counts zero)."""
+    """A workspace for lsa_prefix_decode_attn (it needs no initialisation)."""
     n = int(_load().lsa_prefix_attn_workspace_size(int(B), int(n_groups)))
     if n == 0:
         raise ValueError("unsupported batch")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _groups_fit(prefix_table, cu_group, prefix_len, dev: int) -> bool:
+    return (_fits(prefix_table, torch.int32, dev) and prefix_table.dim() == 2 and _fits(cu_group, torch.int32, dev)
+            and cu_group.numel() == prefix_table.shape[0] + 1 and _fits(prefix_len, torch.int32, dev)
+            and prefix_len.numel() == prefix_table.shape[0])
 
 
 def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len, chunk_table, suffix_len, out, workspace,
@@ -715,25 +805,31 @@ def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len
 
     q and out [B, 64, 128] bf16; prefix_table, cu_group and prefix_len None: no sequence has a prefix; chunk_table
     None: the identity layout with ``max_chunks`` chunks per sequence.  Workspace from new_prefix_attn_workspace."""
-    n_slots, B, max_chunks = _pool_attn_args(q, k_pool, v_pool, chunk_table, suffix_len, max_chunks, out, workspace,
-                                             "suffix_len")
+    dev = _current_device()
+    if not _is(_pool_attn_fits, q, k_pool, v_pool, chunk_table, suffix_len, max_chunks, out, workspace, dev):
+        _pool_attn_explain(q, k_pool, v_pool, chunk_table, suffix_len, max_chunks, out, workspace, "suffix_len")
+    B = suffix_len.numel()
     if q.shape[0] != B:
         raise ValueError("q must be [B, 64, 128]")
     groups = chunks = 0
     if prefix_table is not None:
-        for t, n in ((prefix_table, "prefix_table"), (cu_group, "cu_group"), (prefix_len, "prefix_len")):
-            _need(t, n, torch.int32)
-        if prefix_table.dim() != 2:
-            raise ValueError("prefix_table must be [n_groups, max_prefix_chunks]")
+        if not _is(_groups_fit, prefix_table, cu_group, prefix_len, dev):
+            for t, n in ((prefix_table, "prefix_table"), (cu_group, "cu_group"), (prefix_len, "prefix_len")):
+                _need(t, n, torch.int32)
+            _here(prefix_table, cu_group, prefix_len)
+            raise ValueError("prefix_table must be [n_groups, max_prefix_chunks], cu_group [n_groups + 1] and "
+                             "prefix_len [n_groups]")
         groups, chunks = prefix_table.shape
-        if cu_group.numel() != groups + 1 or prefix_len.numel() != groups:
-            raise ValueError("cu_group must be [n_groups + 1] and prefix_len [n_groups]")
-        _here(prefix_table, cu_group, prefix_len)
-    scale = 1.0 / math.sqrt(HEAD_DIM) if softmax_scale is None else float(softmax_scale)
-    _check("lsa_prefix_decode_attn", _load().lsa_prefix_decode_attn(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), n_slots, _ptr(prefix_table), _ptr(cu_group), _ptr(prefix_len), groups, chunks,
-        _ptr(chunk_table), _ptr(suffix_len), B, max_chunks, scale, _ptr(out), _ptr(workspace), workspace.numel(),
-        _stream(stream)))
+    elif cu_group is not None or prefix_len is not None:
+        raise ValueError("prefix_table, cu_group and prefix_len go together")
+    st = (_lib or _load()).lsa_prefix_decode_attn(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], _at(prefix_table), _at(cu_group),
+        _at(prefix_len), groups, chunks, _at(chunk_table), suffix_len.data_ptr(), B,
+        max_chunks if chunk_table is None else chunk_table.shape[1],
+        _ATTN_SCALE if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream_of(stream, dev))
+    if st:
+        raise LsaError("lsa_prefix_decode_attn", st)
 
 
 from .rope import rope_frequencies  # noqa: E402

@@ -60,7 +60,7 @@ def test_workspace_sizes(L):
     assert w(0, 1) == w(4097, 1) == w(1, 0) == 0
     # two records for each of 160 CTAs' two shares: rows of 128 floats and a log-sum-exp
     assert 0 < w(1, 1) - 4 * 160 * 8 * 129 * 4 < 1 << 16
-    assert w(1, 32) == w(4096, 1 << 20) and w(1, 31) < w(1, 32)
+    assert w(1, 1) < w(1, 8) < w(1, 9) == w(4096, 1 << 20)
     x = L.lsa_prefix_attn_workspace_size
     assert x(0, 0) == x(4097, 1) == x(1, 2) == x(1, -1) == 0
     assert 0 < x(4, 1) < x(5, 1) < x(64, 64)
