@@ -75,7 +75,7 @@ constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
 #endif
 constexpr int kTileCost = TILE_COST;
 #ifndef MIN_SHARE
-#define MIN_SHARE 6
+#define MIN_SHARE 4
 #endif
 constexpr int kMinShare = MIN_SHARE;         // smallest share of a list worth a pipeline (or a CTA) of its own
 constexpr int kFmaEvery = 4;                 // of the pairs of powers of two, one in 4 on the FMA pipe
@@ -99,9 +99,9 @@ struct Plan {
 // call.  Each has only its own code: the softmax loop has no registers to spare.
 enum Mode { kWindowNarrow, kWindow, kPrefixes };
 
-// Partials.  The first and the last segment of a share can be part of a tile:
-// share c has two records, slots 2c and 2c + 1, of as many rows as its kind of
-// tile has.  In prefix mode the rows of a whole tile have places of their own,
+// Partials.  A share can hold the end, or a middle, of a tile that began in an
+// earlier one, and the start of a tile that goes on in the next: share c has a
+// slot for each, 2c and 2c + 1, of as many rows as its kind of tile has.  In prefix mode the rows of a whole tile have places of their own,
 // 64 per sequence for its prefix and 64 for its own tokens, since a sequence's
 // output joins both.  Place says how a query's rows lie there.
 struct Work {
@@ -112,16 +112,15 @@ struct Work {
   int block_rows[2]; // rows of one of its blocks
   int* count;        // kWindowNarrow: [2 kMaxCtas][2 warps], by a tile's first share: units that
                      // its partials hold so far, zero between calls
-  int4* parts;       // kWindow: by slot (wide, then narrow), its tile: first query, KV head and
-                     // queries, first and last share, slot of the first share's partial + 1 (0: none)
+  int4* parts;       // kWindow: by slot (wide, then narrow), its tile: first query, KV head,
+                     // first and last share, queries (0: no partial)
   int* ends;         // prefix mode: [4][8 B], by (sequence, KV head): first and last partial of the
                      // prefix, of the own tokens
   int* ok;           // prefix mode: the offsets were valid
 };
-// The first partial of a (sequence, KV head): its share, slot 2c + bit, whether
-// of the wide list, the query's block and number there, or that the rows are
+// The first partial of a (sequence, KV head): its share, whether of the wide list, the query's block and number there, or that the rows are
 // in their own place; kNone: no partial.
-constexpr int kEndShare = 0x3ff, kEndSlot = 1 << 10, kEndWide = 1 << 11, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
+constexpr int kEndShare = 0x3ff, kEndWide = 1 << 11, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
 
 // The queries and the keys of one list entry: a sequence, or a group over its prefix.
 struct List {
@@ -662,9 +661,8 @@ struct Seg {
   int first, low;            // chunk of unit j: j < first ? j : low + j - first
   int f0, f1, f2;            // units that every query sees whole: j < f0 and f1 <= j <= f2
   int p0, len;               // window mode: position of the first query; prefix mode: tokens
-  int share, index;          // the share, the segment's index in it
+  int slot;                  // of its partial
   int lo, hi;                // window mode: first and last share of the tile
-  int slot0;                 // window mode: the slot of the first share's partial
   int all;                   // units of the tile
   int g;
   const int32_t* table;
@@ -898,8 +896,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             s->f2 = f2;
             s->p0 = cur.p0;
             s->len = cur.s.len;
-            s->share = share;
-            s->index = put;
+            s->slot = 2 * share + (begins ? 1 : 0);
             s->all = cur.n;
             s->g = cur.g;
             s->table = cur.s.table;
@@ -911,7 +908,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (lane == 0) {
               s->lo = lo;
               s->hi = hi;
-              s->slot0 = 2 * lo + (part.start(lo) >= cur.at ? 0 : 1);   // there it may come after other tiles
             }
           }
         }
@@ -925,8 +921,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               const int lo = begins ? share : part.share_of(cur.at + kTileCost);
               const int hi = ends ? share : part.share_of(cur.at + kTileCost + cur.n - 1);
               if (lane == 0)
-                work.parts[(wide ? 0 : 2 * kMaxCtas) + 2 * share + (put ? 1 : 0)] =
-                    make_int4(cur.row(wide), cur.g | (cur.cnt << 8), lo | (hi << 16), 2 * lo + (part.start(lo) >= cur.at ? 0 : 1) + 1);
+                work.parts[(wide ? 0 : 2 * kMaxCtas) + 2 * share + (begins ? 1 : 0)] =
+                    make_int4(cur.row(wide), cur.g, lo | (hi << 16), cur.cnt);
             }
           }
           more = cur.next(plan, wide);
@@ -1315,7 +1311,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
           } else {
             const Place at_o = whole ? own_place(work, plan.B, row0 + (lane >> 3), head >> 3, !(sg.flags & kSegGroup))
-                                     : slot_place(work, wide, 2 * sg.share + (sg.index > 0), wide ? warp : wq, lane >> 3);
+                                     : slot_place(work, wide, sg.slot, wide ? warp : wq, lane >> 3);
             float* const to = work.o + at_o.o + (lane & 7) * 4;
             const bool valid = (lane >> 3) < queries;
 #pragma unroll 1
@@ -1344,10 +1340,10 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (__shfl_sync(0xffffffffu, before, 0) + n == sg.all) {
               if (lane == 0) *count = 0;
               __threadfence();
-              const int lo = sg.lo, slot0 = sg.slot0;
+              const int lo = sg.lo;
               for (int i = 0; i < queries; ++i)
                 fold_query(work, sg.hi - lo + 1, lane,
-                           [&](int x) { return slot_place(work, 0, x == 0 ? slot0 : 2 * (lo + x), wq, i); },
+                           [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), wq, i); },
                            out + (static_cast<int64_t>(row0 + i) * kNumQHeads + head) * kHeadDim);
             }
           }
@@ -1356,9 +1352,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             int* const ends = work.ends + (row0 + lane) * kNumKVHeads + (head >> 3);
             if (j0 == 0)
               ends[part * pairs] = final ? kNone
-                                         : sg.share | (sg.index > 0 ? kEndSlot : 0) | (wide ? kEndWide : 0) |
+                                         : (sg.slot >> 1) | (wide ? kEndWide : 0) |
                                                (((wide ? warp : wq) * 4 + lane) << kEndPlace) | (whole ? kEndWhole : 0);
-            if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.share;
+            if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.slot >> 1;
             if (sg.flags & kSegAlone) ends[0] = kNone;
           }
         }
@@ -1405,13 +1401,13 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Work 
     const uint4 a = parts[x];
     if (!a.w) continue;
     const int share = x < 2 ? blockIdx.x : 2 * blockIdx.x + ((x - 2) >> 1), wide = x < 2;
-    const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.y >> 8);
+    const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
     const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
     for (int q = share - lo + n * warp; q < cnt; q += n * kMergeWarps) {
       const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
       fold_query(work, n, lane,
-                 [&](int k) { return slot_place(work, wide, k == 0 ? static_cast<int>(a.w) - 1 : 2 * (lo + k), block, i & 3); },
-                 out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + (a.y & 0xff) * kGroup) * kHeadDim);
+                 [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); },
+                 out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + static_cast<int>(a.y) * kGroup) * kHeadDim);
     }
   }
 }
@@ -1439,7 +1435,7 @@ __global__ void __launch_bounds__(kPrefixMergeThreads) prefix_merge_kernel(const
                if (own) i -= n0;
                if (first & kEndWhole) return own_place(work, B, pair / kNumKVHeads, pair % kNumKVHeads, own);
                return slot_place(work, first & kEndWide ? 1 : 0,
-                                 2 * ((first & kEndShare) + i) + (i == 0 && (first & kEndSlot) ? 1 : 0),
+                                 2 * ((first & kEndShare) + i) + (i == 0),
                                  (first >> (kEndPlace + 2)) & 7, (first >> kEndPlace) & 3);
              },
              out + static_cast<int64_t>(pair) * kGroup * kHeadDim);
