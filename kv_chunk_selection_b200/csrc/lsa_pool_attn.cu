@@ -70,14 +70,8 @@ constexpr int kQ2Bytes = 8192;               // a pipeline's second narrow query
 constexpr int kTurnBytes = 4096;             // a warp's rows on their way out: 32 rows x 128 bytes
 constexpr int kAhead = 4;                    // places for segments that a planner is ahead
 constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
-#ifndef TILE_COST
-#define TILE_COST 3
-#endif
-constexpr int kTileCost = TILE_COST;
-#ifndef MIN_SHARE
-#define MIN_SHARE 4
-#endif
-constexpr int kMinShare = MIN_SHARE;         // smallest share of a list worth a pipeline (or a CTA) of its own
+constexpr int kTileCost = 3;                 // 2 to 5 measured alike
+constexpr int kMinShare = 4;                 // smallest share of a list worth a pipeline (or a CTA) of its own: 3 to 8 alike
 constexpr int kFmaEvery = 4;                 // of the pairs of powers of two, one in 4 on the FMA pipe
 constexpr float kRaise = 8.f;                // growth of the maximum (log2) that rescales the accumulator
 constexpr int kSCols = 64, kOCol0 = 256;     // TMEM: S[w][b] at (2 w + b) * 64, O[w] at 256 + 128 w
@@ -341,6 +335,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity) {
       : "memory");
   return ok != 0;
 }
+// Whether the phase has completed, at once: try_wait may sleep for a while first,
+// which a caller that has something else to do must not.
+__device__ __forceinline__ bool bar_test(uint32_t bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Waits, at most kWaitLimitNs, or until another role has given up; the same
 // answer in every lane, so that the warp's collective instructions stay whole.
 // `abort_flag`: 0, or 1 once a wait of the CTA ran out.
@@ -591,13 +596,13 @@ __device__ __forceinline__ Place own_place(const Work& w, int B, int b, int g, b
 }
 
 // The 8 rows of a query: joins its n partials at place(0) .. place(n - 1), in
-// that order, and writes the output.  A warp; lane i has row i % 8 and the dims
-// 4 c .. 4 c + 3 with c % 4 = i / 8.  The loads of 4 partials are in flight
-// together.
-template <typename At>
-__device__ __forceinline__ void fold_query(const Work& w, int n, int lane, At place, __nv_bfloat16* out) {
-  constexpr int kBatch = 4, kPieces = kHeadDim / 16;
-  const int h = lane & 7, c0 = lane >> 3;
+// that order, and writes part `part` of kParts of the output's dims.  A warp;
+// lane i has row i % 8 and the dims 4 c .. 4 c + 3 with c % 4 = i / 8.  The loads
+// of 4 kParts partials are in flight together.
+template <int kParts, typename At>
+__device__ __forceinline__ void fold_query(const Work& w, int n, int lane, At place, __nv_bfloat16* out, int part = 0) {
+  constexpr int kBatch = 4 * kParts, kPieces = kHeadDim / 16 / kParts;
+  const int h = lane & 7, c0 = (lane >> 3) + 4 * kPieces * part;
   float m = -INFINITY, den = 0.f;
   float4 acc[kPieces];
 #pragma unroll
@@ -1087,7 +1092,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (; next < min(n, i + 2); ++next) {
               const unsigned kx = 2 * (at + next), h = ring.half(kx), jb = job + next, buf = jb & 1;
               if (next > i) {
-                if (!__all_sync(0xffffffffu, bar_try(sm + kFull + 8 * h, ring.parity(kx)))) break;
+                if (!__all_sync(0xffffffffu, bar_test(sm + kFull + 8 * h, ring.parity(kx)))) break;
               } else {
                 ok = wait(kFull + 8 * h, ring.parity(kx));
               }
@@ -1342,7 +1347,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               __threadfence();
               const int lo = sg.lo;
               for (int i = 0; i < queries; ++i)
-                fold_query(work, sg.hi - lo + 1, lane,
+                fold_query<1>(work, sg.hi - lo + 1, lane,
                            [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), wq, i); },
                            out + (static_cast<int64_t>(row0 + i) * kNumQHeads + head) * kHeadDim);
             }
@@ -1381,7 +1386,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // ---- the merge kernels --------------------------------------------------------
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kPrefixMergeThreads = 64;
 
 // Window mode: CTA c looks at the tiles that share c of the wide list, and
 // shares 2c and 2c + 1 of the narrow one, began or ended with; the rows of a
@@ -1405,20 +1409,21 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Work 
     const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
     for (int q = share - lo + n * warp; q < cnt; q += n * kMergeWarps) {
       const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
-      fold_query(work, n, lane,
+      fold_query<1>(work, n, lane,
                  [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); },
                  out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + static_cast<int>(a.y) * kGroup) * kHeadDim);
     }
   }
 }
 
-// Prefix mode: a warp per (sequence, KV head): the partials of its group's tile,
-// then those of its own tokens.
-__global__ void __launch_bounds__(kPrefixMergeThreads) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
+// Prefix mode: a CTA of 4 warps per (sequence, KV head), a quarter of the dims
+// each: the partials of its group's tile, then those of its own tokens.
+constexpr int kFoldParts = 4;
+__global__ void __launch_bounds__(32 * kFoldParts) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int pairs = B * kNumKVHeads, pair = blockIdx.x * (kPrefixMergeThreads / 32) + (threadIdx.x >> 5);
+  const int pairs = B * kNumKVHeads, pair = blockIdx.x;
   const int ok = ld_dep(work.ok);
   int ends[4];
 #pragma unroll
@@ -1428,7 +1433,7 @@ __global__ void __launch_bounds__(kPrefixMergeThreads) prefix_merge_kernel(const
     return first == kNone ? 0 : first & kEndWhole ? 1 : last - (first & kEndShare) + 1;
   };
   const int n0 = many(ends[0], ends[1]), n1 = many(ends[2], ends[3]);
-  fold_query(work, n0 + n1, lane,
+  fold_query<kFoldParts>(work, n0 + n1, lane,
              [&](int i) {
                const bool own = i >= n0;
                const int first = own ? ends[2] : ends[0];
@@ -1438,7 +1443,7 @@ __global__ void __launch_bounds__(kPrefixMergeThreads) prefix_merge_kernel(const
                                  2 * ((first & kEndShare) + i) + (i == 0),
                                  (first >> (kEndPlace + 2)) & 7, (first >> kEndPlace) & 3);
              },
-             out + static_cast<int64_t>(pair) * kGroup * kHeadDim);
+             out + static_cast<int64_t>(pair) * kGroup * kHeadDim, threadIdx.x >> 5);
 }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
@@ -1543,8 +1548,8 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
-    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads * 32 / kPrefixMergeThreads),
-               dim3(kPrefixMergeThreads), 0, s, work, plan.B, o);
+    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work,
+               plan.B, o);
   else if (kMode == kWindow)
     launch_pdl(true, window_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, s, work, o);
   return launch_status();
