@@ -598,10 +598,10 @@ __device__ __forceinline__ Place own_place(const Work& w, int B, int b, int g, b
 // The 8 rows of a query: joins its n partials at place(0) .. place(n - 1), in
 // that order, and writes part `part` of kParts of the output's dims.  A warp;
 // lane i has row i % 8 and the dims 4 c .. 4 c + 3 with c % 4 = i / 8.  The loads
-// of 4 kParts partials are in flight together.
-template <int kParts, typename At>
+// of kBatch partials are in flight together.
+template <int kParts, int kBatch, typename At>
 __device__ __forceinline__ void fold_query(const Work& w, int n, int lane, At place, __nv_bfloat16* out, int part = 0) {
-  constexpr int kBatch = 4 * kParts, kPieces = kHeadDim / 16 / kParts;
+  constexpr int kPieces = kHeadDim / 16 / kParts;
   const int h = lane & 7, c0 = (lane >> 3) + 4 * kPieces * part;
   float m = -INFINITY, den = 0.f;
   float4 acc[kPieces];
@@ -1347,7 +1347,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               __threadfence();
               const int lo = sg.lo;
               for (int i = 0; i < queries; ++i)
-                fold_query<1>(work, sg.hi - lo + 1, lane,
+                fold_query<1, 4>(work, sg.hi - lo + 1, lane,
                            [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), wq, i); },
                            out + (static_cast<int64_t>(row0 + i) * kNumQHeads + head) * kHeadDim);
             }
@@ -1384,35 +1384,30 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // ---- the merge kernels --------------------------------------------------------
-constexpr int kMergeThreads = 256;
-constexpr int kMergeWarps = kMergeThreads / 32;
-
-// Window mode: CTA c looks at the tiles that share c of the wide list, and
-// shares 2c and 2c + 1 of the narrow one, began or ended with; the rows of a
-// split tile are shared out over the shares that it was split over.
-__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Work work, __nv_bfloat16* __restrict__ out) {
+// Window mode.  The queries of a split tile are shared out over the slots that
+// hold its partials.  CTA (x, y) for x below 2 grid: slot x of the wide shares, 2
+// warps (half the dims each) to a query, 16 queries of a tile in two parts at
+// once over y; further x: a warp to each slot of the narrow shares.  (A CTA of 8
+// warps per share took 20 us more at 4096 tokens.)
+constexpr int kMergeWarps = 8, kMergeY = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint4 parts[6];
-#pragma unroll
-  for (int x = 0; x < 6; ++x) {
-    const int slot = x < 2 ? 2 * blockIdx.x + x : 2 * kMaxCtas + 4 * blockIdx.x + x - 2;
-    parts[x] = ld_dep(reinterpret_cast<const uint4*>(work.parts + slot));
-  }
-#pragma unroll
-  for (int x = 0; x < 6; ++x) {
-    const uint4 a = parts[x];
-    if (!a.w) continue;
-    const int share = x < 2 ? blockIdx.x : 2 * blockIdx.x + ((x - 2) >> 1), wide = x < 2;
-    const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
-    const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
-    for (int q = share - lo + n * warp; q < cnt; q += n * kMergeWarps) {
-      const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
-      fold_query<1>(work, n, lane,
-                 [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); },
-                 out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + static_cast<int>(a.y) * kGroup) * kHeadDim);
-    }
+  const int wide = static_cast<int>(blockIdx.x) < 2 * grid;
+  const int slot = wide ? blockIdx.x : (blockIdx.x - 2 * grid) * kMergeWarps + warp;
+  if (!wide && (blockIdx.y || slot >= 4 * grid)) return;
+  const uint4 a = ld_dep(reinterpret_cast<const uint4*>(work.parts + (wide ? 0 : 2 * kMaxCtas) + slot));
+  if (!a.w) return;
+  const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
+  const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
+  const int first = wide ? blockIdx.y * (kMergeWarps / 2) + (warp >> 1) : 0, step = wide ? kMergeY * kMergeWarps / 2 : 1;
+  for (int q = (slot >> 1) - lo + n * first; q < cnt; q += n * step) {
+    const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
+    const auto at = [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); };
+    __nv_bfloat16* const to = out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + static_cast<int>(a.y) * kGroup) * kHeadDim;
+    fold_query<2, 4>(work, n, lane, at, to, wide ? warp & 1 : 0);
+    if (!wide) fold_query<2, 4>(work, n, lane, at, to, 1);
   }
 }
 
@@ -1433,7 +1428,7 @@ __global__ void __launch_bounds__(32 * kFoldParts) prefix_merge_kernel(const Wor
     return first == kNone ? 0 : first & kEndWhole ? 1 : last - (first & kEndShare) + 1;
   };
   const int n0 = many(ends[0], ends[1]), n1 = many(ends[2], ends[3]);
-  fold_query<kFoldParts>(work, n0 + n1, lane,
+  fold_query<kFoldParts, 16>(work, n0 + n1, lane,
              [&](int i) {
                const bool own = i >= n0;
                const int first = own ? ends[2] : ends[0];
@@ -1551,7 +1546,8 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
     launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work,
                plan.B, o);
   else if (kMode == kWindow)
-    launch_pdl(true, window_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, s, work, o);
+    launch_pdl(true, window_merge_kernel, dim3(2 * grid + (4 * grid + kMergeWarps - 1) / kMergeWarps, kMergeY),
+               dim3(32 * kMergeWarps), 0, s, work, grid, o);
   return launch_status();
 }
 
