@@ -271,15 +271,17 @@ struct Cursor {
     r -= g * per_head;
     // The last tile that starts at or before r, 32 ways at a time.
     int lo = 0, n = tiles;
+    int64_t before = 0;
     while (n > 1) {
-      const int step = (n + 31) / 32, i = lo + lane * step;
-      const unsigned at_or_before = __ballot_sync(0xffffffffu, lane * step < n && span<kPrefix>(p, s, wide, i) <= r);
-      const int k = 31 - __clz(at_or_before);   // lane 0's is
+      const int step = (n + 31) / 32;
+      const int64_t x = lane * step < n ? span<kPrefix>(p, s, wide, lo + lane * step) : r + 1;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, x <= r));   // lane 0's is
+      before = __shfl_sync(0xffffffffu, x, k);
       n = min(step, n - k * step);
       lo += k * step;
     }
     t = lo;
-    r -= span<kPrefix>(p, s, wide, t);
+    r -= before;
     at = u - r;
     j = max(0, static_cast<int>(r) - kTileCost);
     set_tile(p, wide);
@@ -864,7 +866,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           more = cur.units() > 0;
         }
       };
-      // Writes the next segment of share x, or its end.
+      // Writes the next segment of share x, or its end; `advance` follows.
       auto publish = [&](int x, const Partition& part, int share) {
         const int place = x * kAhead + put % kAhead;
         if (put >= kAhead && !wait(kSegDone + 8 * place, (put / kAhead - 1) & 1)) return false;
@@ -918,6 +920,10 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         __syncwarp();
         if (lane == 0) bar_arrive(sm + kSegFull + 8 * place);
+        ++put;
+        return true;
+      };
+      auto advance = [&](int x, const Partition& part, int share) {
         if (more) {
           const bool wide = x == 0;
           if (kMode == kWindow) {   // what the merge has to know
@@ -932,8 +938,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           }
           more = cur.next(plan, wide);
         }
-        ++put;
-        return true;
       };
       const uint64_t policy_once = l2_policy_evict_first(), policy_again = l2_policy_evict_normal();
       const int beyond = static_cast<int>(plan.n_slots) * (kNumKVHeads * kChunkTokens);   // reads as zeros
@@ -969,6 +973,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               load_box(dst + kBoxBytes, map, 64, y, bar, policy);
             }
             __syncwarp();
+            // A wide share's first K comes alone: every CTA starts at once, and with
+            // the whole ring asked for together the first products would wait 4 us.
+            if (ring.mask == 7 && x == 0 && kv == 0 && !wait(kFull + 8 * h, 0)) return false;
           }
         }
         return true;
@@ -1013,7 +1020,10 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             __syncwarp();
           }
-          while (ok && !ended && put < k + kAhead) ok = publish(0, part_w, me);
+          while (ok && !ended && put < k + kAhead) {   // (after the first segment's query tiles)
+            advance(0, part_w, me);
+            ok = publish(0, part_w, me);
+          }
         }
         for (int t = 0; ok && k && t < 2; ++t) ok = wait(kQEmpty + 8 * t, (k - 1) & 1);
         if (ok && lane == 0) bar_arrive(sm + kHandOver);
@@ -1049,6 +1059,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         ++loads;
         ok = load_units(ring, x, units, flags, j0, first, low, g, table, ident);
         x += units;
+        advance(1 + w, part_n, 2 * me + w);
       }
       if (!ok && lane == 0) {   // copies in flight land before the CTA ends
         volatile int never = 0;
