@@ -833,6 +833,11 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const uint32_t tmem = *reinterpret_cast<const volatile uint32_t*>(smem + kTmemAt);
   const Seg* const segs = reinterpret_cast<const Seg*>(smem + kSegAt);
   auto wait = [&](int bar, unsigned parity) { return bar_wait(sm + bar, parity, abort_flag, status); };
+  // Two at once: a barrier that is ready still costs its round trip.
+  auto wait2 = [&](int a, unsigned parity_a, int b, unsigned parity_b) {
+    const bool ready_a = bar_try(sm + a, parity_a), ready_b = bar_try(sm + b, parity_b);
+    return __all_sync(0xffffffffu, ready_a && ready_b) || (wait(a, parity_a) && wait(b, parity_b));
+  };
   // Segment k of share x (0: wide, 1 + w: narrow); its place is free again once
   // every role has said so.
   auto seg_get = [&](int x, unsigned k) { return wait(kSegFull + 8 * (x * kAhead + k % kAhead), (k / kAhead) & 1); };
@@ -1095,19 +1100,17 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const int q_empty = x == 0 ? kQEmpty + 8 * w : kNEmpty + 16 * w + 8 * (k & 1);
           const uint32_t q_lo = q_lo0 + (x == 0 ? 0 : (k & 1) * (kQ2Bytes >> 4));
           ok = wait(q_full, (x == 0 ? k : k >> 1) & 1);
-          // Scores run up to two units (both buffers) before the products, as far
-          // as units have arrived: waiting for one that has not would hold back
-          // the product that frees a half-stage.
+          // Scores run up to two units (both buffers) before the products: in the
+          // narrow share as far as units have arrived, since waiting for one that
+          // has not would hold back the product that frees a half-stage.
           int next = 0;
           for (int i = 0; ok && i < n; ++i) {
             for (; next < min(n, i + 2); ++next) {
               const unsigned kx = 2 * (at + next), h = ring.half(kx), jb = job + next, buf = jb & 1;
-              if (next > i) {
-                if (!__all_sync(0xffffffffu, bar_test(sm + kFull + 8 * h, ring.parity(kx)))) break;
-              } else {
-                ok = wait(kFull + 8 * h, ring.parity(kx));
-              }
-              if (ok && jb >= 2) ok = wait(o_bar + 8 * buf, ((jb - 2) >> 1) & 1);   // the buffer's probabilities are read
+              if (x && next > i && !__all_sync(0xffffffffu, bar_test(sm + kFull + 8 * h, ring.parity(kx)))) break;
+              // K is there, and the buffer's probabilities have been read.
+              ok = jb < 2 ? wait(kFull + 8 * h, ring.parity(kx))
+                          : wait2(kFull + 8 * h, ring.parity(kx), o_bar + 8 * buf, ((jb - 2) >> 1) & 1);
               if (!ok) break;
               tcgen05_fence_after();
               const uint32_t k_lo = k_lo0 + h * (kHalfBytes >> 4), d = s_col0 + buf * kSCols;
@@ -1122,7 +1125,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             if (!ok) break;
             const unsigned vx = 2 * (at + i) + 1, h = ring.half(vx), jb = job + i, buf = jb & 1;
-            ok = wait(kFull + 8 * h, ring.parity(vx)) && wait(p_bar + 8 * buf, (jb >> 1) & 1);
+            ok = wait2(kFull + 8 * h, ring.parity(vx), p_bar + 8 * buf, (jb >> 1) & 1);
             if (!ok) break;
             tcgen05_fence_after();
             const uint32_t v_lo = v_lo0 + h * (kHalfBytes >> 4), a = s_col0 + buf * kSCols;
