@@ -660,7 +660,7 @@ int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const 
  *               16-byte aligned, zero before the first call (and again after a
  *               call that reported TIMEOUT): every call leaves the counts in it
  *               zero.  Calls that may overlap on the GPU need workspaces of
- *               their own, and a workspace serves one max_q (its layout)
+ *               their own
  * K and V rows that no query of a sequence sees may hold anything, NaN
  * included; a value of V that is not finite and that one query sees may reach
  * the other queries of the same 32 (a prompt's) that do not.

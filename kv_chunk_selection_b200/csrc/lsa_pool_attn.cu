@@ -21,7 +21,7 @@
 // a long window, a ragged batch and a long prompt all fill the chip evenly.  A
 // tile that a cut splits leaves partials (normalised rows and their
 // log-sum-exps), which are folded in the order of the shares, so that the result
-// does not depend on timing: by the warp that adds a tile's last one where a
+// does not depend on timing: by the share that adds a tile's last one where a
 // window call has narrow tiles only (no second launch), else by a second kernel
 // (the partials of wide tiles are too many for one SM: 32 sequences over a
 // prefix of 32768 tokens leave 19 MB).
@@ -71,7 +71,8 @@ constexpr int kTurnBytes = 4096;             // a warp's rows on their way out: 
 constexpr int kAhead = 4;                    // places for segments that a planner is ahead
 constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
 constexpr int kTileCost = 3;                 // 2 to 5 measured alike
-constexpr int kMinShare = 4;                 // smallest share of a list worth a pipeline (or a CTA) of its own: 3 to 8 alike
+constexpr int kMinShare = 3;                 // smallest share of a list worth a pipeline (or a CTA) of its own: one token
+                                             // over 4096 takes 16.6 us with 2, 16.0 with 3, 16.2 with 4, 16.8 with 6
 constexpr int kFmaEvery = 4;                 // of the pairs of powers of two, one in 4 on the FMA pipe
 constexpr float kRaise = 8.f;                // growth of the maximum (log2) that rescales the accumulator
 constexpr int kSCols = 64, kOCol0 = 256;     // TMEM: S[w][b] at (2 w + b) * 64, O[w] at 256 + 128 w
@@ -104,8 +105,8 @@ struct Work {
   int64_t slots[2];  // first row of the narrow slots, of the wide ones
   int rows[2];       // rows of a narrow slot, of a wide one
   int block_rows[2]; // rows of one of its blocks
-  int* count;        // kWindowNarrow: [2 kMaxCtas][2 warps], by a tile's first share: units that
-                     // its partials hold so far, zero between calls
+  int* count;        // kWindowNarrow: [2 kMaxCtas], by a tile's first share: units that its partials
+                     // hold so far, zero between calls
   int4* parts;       // kWindow: by slot (wide, then narrow), its tile: first query, KV head,
                      // first and last share, queries (0: no partial)
   int* ends;         // prefix mode: [4][8 B], by (sequence, KV head): first and last partial of the
@@ -689,15 +690,15 @@ constexpr int kQFull = kODone + 32, kQEmpty = kQFull + 16;             // [2] qu
 constexpr int kNFull = kQEmpty + 16, kNEmpty = kNFull + 32;            // [2 pipelines][2] of the narrow ones
 constexpr int kSegFull = kNEmpty + 32, kSegDone = kSegFull + 24 * kAhead;   // [3][kAhead]
 constexpr int kHandOver = kSegDone + 24 * kAhead;                      // [2]: 11's part of the wide share is done, 10's is
-constexpr int kDrain = kHandOver + 16;                                 // [2]
-constexpr int kTmemAt = kDrain + 16, kAbortAt = kTmemAt + 4;
+constexpr int kDrain = kHandOver + 16, kMeet = kDrain + 16;            // [2], [2]: a warpgroup's warps
+constexpr int kTmemAt = kMeet + 16, kAbortAt = kTmemAt + 4, kVerdictAt = kAbortAt + 4;   // (two verdicts)
 // The entry at the start of the wide share and of the two narrow ones.
 struct Found {
   List s;
   int64_t r, per_head;       // the place in the entry, the entry's places per KV head
   int v;
 };
-constexpr int kFoundAt = kAbortAt + 4;
+constexpr int kFoundAt = kVerdictAt + 8;
 constexpr int kSmemBytes = kFoundAt + 3 * static_cast<int>(sizeof(Found));
 static_assert(kSmemBytes <= 232448 && sizeof(Seg) % 8 == 0 && kFoundAt % 8 == 0, "shared memory of one CTA");
 
@@ -751,6 +752,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       bar_init(sm + kQEmpty + 8 * i, 1);
       bar_init(sm + kHandOver + 8 * i, 1);
       bar_init(sm + kDrain + 8 * i, 1);
+      bar_init(sm + kMeet + 8 * i, 4);
     }
     for (int i = 0; i < 3 * kAhead; ++i) {
       bar_init(sm + kSegFull + 8 * i, 1);
@@ -1153,8 +1155,14 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t s_col0 = tmem + 2 * w * kSCols + lanes, o_col0 = tmem + kOCol0 + w * kHeadDim + lanes;
     const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
     const uint64_t scale2 = pack2(scale_log2, scale_log2);
-    unsigned job = 0, wide_units = 0;
+    unsigned job = 0, wide_units = 0, meets = 0;
     bool ok = true;
+    // The warps of the warpgroup.
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) bar_arrive(sm + kMeet + 8 * w);
+      return wait(kMeet + 8 * w, meets++ & 1);
+    };
 #pragma unroll 1
     for (int share = kHasWide ? 0 : 1 + w; ok && share <= 1 + w; share += 1 + w) {
       const bool wide = share == 0;
@@ -1348,24 +1356,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (valid) work.lse[at_o.lse + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
           }
           tcgen05_fence_before();
-          if (kFold && !final) {
-            // Few queries a sequence: the warp that adds a tile's last units folds
-            // its rows (the other shares' are from the same warp there).
-            int* const count = work.count + sg.lo * 2 + wq;
-            int before = 0;
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) before = atomicAdd(count, n);
-            if (__shfl_sync(0xffffffffu, before, 0) + n == sg.all) {
-              if (lane == 0) *count = 0;
-              __threadfence();
-              const int lo = sg.lo;
-              for (int i = 0; i < queries; ++i)
-                fold_query<1, 4>(work, sg.hi - lo + 1, lane,
-                           [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), wq, i); },
-                           out + (static_cast<int64_t>(row0 + i) * kNumQHeads + head) * kHeadDim);
-            }
-          }
           if (kPrefix && lane < queries) {   // where the merge finds the partials
             const int part = (sg.flags & kSegGroup) ? 0 : 2, pairs = plan.B * kNumKVHeads;
             int* const ends = work.ends + (row0 + lane) * kNumKVHeads + (head >> 3);
@@ -1375,6 +1365,31 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                                (((wide ? warp : wq) * 4 + lane) << kEndPlace) | (whole ? kEndWhole : 0);
             if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.slot >> 1;
             if (sg.flags & kSegAlone) ends[0] = kNone;
+          }
+        }
+        if (kFold && !(sg.flags & kSegWhole)) {
+          // Few queries a sequence: the share that adds a tile's last units folds
+          // its rows, a quarter of the dims a warp.
+          int* const verdict = reinterpret_cast<int*>(smem + kVerdictAt) + w;
+          __threadfence();
+          ok = meet();                               // the partial is written
+          if (!ok) break;
+          if (wq == 0 && lane == 0) {
+            int* const count = work.count + sg.lo;
+            __threadfence();
+            const bool last = atomicAdd(count, n) + n == sg.all;
+            if (last) *count = 0;
+            *verdict = last;
+          }
+          ok = meet();
+          if (!ok) break;
+          if (*verdict) {
+            __threadfence();
+            const int lo = sg.lo, cnt = sg.cnt;
+            for (int i = 0; i < cnt; ++i)
+              fold_query<4, 12>(work, sg.hi - lo + 1, lane,
+                                [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), i >> 2, i & 3); },
+                                out + ((static_cast<int64_t>(sg.row) + i) * kNumQHeads + sg.head) * kHeadDim, wq);
           }
         }
         tcgen05_fence_before();
@@ -1463,7 +1478,7 @@ size_t layout(Work* w, void* at, int64_t places, int queries, int64_t pairs) {
   const int narrow = kGroup * (queries <= 4 ? queries : kNarrowQ);   // whole blocks of 4 queries, or one smaller block
   const int wide = queries <= kNarrowQ ? 0 : kGroup * kWideQ;
   const int64_t rows = places + 2ll * kMaxCtas * wide + 4ll * kMaxCtas * narrow;
-  const size_t count = 4 * kMaxCtas * sizeof(int), parts = 6 * kMaxCtas * sizeof(int4);
+  const size_t count = 2 * kMaxCtas * sizeof(int), parts = 6 * kMaxCtas * sizeof(int4);
   const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4), ends = round16(4 * pairs * 4), ok = 16;
   if (w) {
     char* p = static_cast<char*>(at);
