@@ -604,7 +604,8 @@ int lsa_gather_tokens(const void* k_buf, const void* v_buf, int64_t buf_chunks, 
  *              multiple of 8
  *   q_out      device bf16 [T][64][128]; k_out, v_out device bf16 [T][8][128]
  *              (v_out may be NULL: the value heads are not copied)
- * The outputs must not overlap qkv.  T > 0.  No device errors.
+ * The outputs must not overlap qkv or one another (the same pointer twice is
+ * LSA_ERR_INVALID_ARG).  T > 0.  No device errors.
  */
 #define LSA_ROPE_INTERLEAVED 1u
 int lsa_qk_norm_rope(const void* qkv, int64_t row_stride, int64_t T, const float* q_weight,

@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const Args a, un
 // Checks and launch shared by both forms.
 int launch(const Args& a, int64_t T, unsigned flags, void* stream) {
   if (!a.qkv || !a.q_out || !a.k_out || T <= 0) return LSA_ERR_INVALID_ARG;
+  if (a.k_out == a.v_out || a.q_out == a.k_out || a.q_out == a.v_out) return LSA_ERR_INVALID_ARG;   // two heads, one place
   if (flags & ~static_cast<unsigned>(LSA_ROPE_INTERLEAVED)) return LSA_ERR_INVALID_ARG;
   if (a.rot_dim < 0 || a.rot_dim > kHeadDim || a.row_stride < kHeadsIn * kHeadDim) return LSA_ERR_INVALID_ARG;
   if (a.rot_dim > 0 && (!a.positions || !a.inv_freq)) return LSA_ERR_INVALID_ARG;

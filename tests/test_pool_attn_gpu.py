@@ -239,3 +239,151 @@ def test_prefix_refuses_bad_offsets_and_reports_lengths_and_slots():
     c.d_table = tab
     assert torch.equal(c.call(), good)
     clean()
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_ragged_batches_of_prompts_and_tokens(seed):
+    """Wide and narrow tiles side by side in one call, at the sizes where a tile changes its kind."""
+    g = torch.Generator().manual_seed(seed)
+    pick = lambda v: v[int(torch.randint(len(v), (1,), generator=g))]  # noqa: E731
+    seqs = []
+    for _ in range(9):
+        nq = pick([1, 1, 2, 7, 8, 9, 16, 31, 32, 33, 40, 41, 63, 64, 65, 73, 129])
+        seqs.append((nq, nq + pick([0, 1, 63, 64, 200, 700])))
+    c = WindowCase(seqs, pick([1, 17, 64, 250, 1 << 20]), pick([0, 1, 64, 100]), seed=seed, spare_rows=5)
+    c.check(c.call())
+    c.check(c.call())
+    clean()
+
+
+def test_one_token_over_a_long_window():
+    c = WindowCase([(1, 20001)], 1 << 20, 0)
+    c.check(c.call())
+    c = WindowCase([(3, 20000), (1, 9000)], 12345, 70)
+    c.check(c.call())
+    clean()
+
+
+def test_a_query_or_key_that_is_not_a_number_reaches_the_rows_that_see_it():
+    c = WindowCase([(40, 200), (1, 150)], 1 << 20, 0)
+    good = c.call()
+    c.d_q[7, 3] = float("nan")                    # query 7, head 3
+    out = c.call()
+    assert bool(out[7, 3].isnan().all())
+    out[7, 3] = good[7, 3]
+    assert torch.equal(out, good)
+    c.d_q.copy_(c.q)
+    c.d_k[int(c.d_table[0, 2]), 5, 52] = float("nan")   # token 180 of sequence 0, KV head 5: seen from query 20 on
+    out = c.call()
+    assert bool(out[20:40, 40:48].isnan().all())
+    assert torch.equal(out[:20], good[:20]) and torch.equal(out[40:], good[40:])
+    assert torch.equal(out[:, :40], good[:, :40]) and torch.equal(out[:, 48:], good[:, 48:])
+    c.d_k.copy_(c.d_k.nan_to_num(0.0))
+    c.d_q[7, 3] = float("inf")                    # infinite scores of both signs
+    assert bool(c.call()[7, 3].isnan().all())
+    clean()
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own():
+    a = WindowCase([(1, 700), (1, 90), (1, 4000)], 1 << 20, 0, seed=1)
+    b = WindowCase([(90, 300), (1, 500)], 128, 4, seed=2)
+    p = PrefixCase([(20, 600)], [(13 * i) % 200 for i in range(25)], seed=3)
+    ref = [x.call() for x in (a, b, p)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for _ in range(10):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        outs.append([x.call(stream=s) for x, s in zip((a, b, p), streams)])
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(x, y) for x, y in zip(o, ref))
+    clean()
+
+
+def test_one_workspace_for_calls_of_both_kinds():
+    """The larger workspace serves a call with few queries too, before and after one with many."""
+    many, few = WindowCase([(70, 400), (1, 300)], 1 << 20, 0), WindowCase([(1, 900), (2, 2000)], 1 << 20, 0)
+    ws = many.ws
+    for _ in range(3):
+        many.check(many.call(workspace=ws))
+        few.check(few.call(workspace=ws))
+    clean()
+
+
+def test_slots_past_32_bit_offsets():
+    """A pool of 2^31 elements and more, its last slots in use."""
+    slots = 33000                                  # 2.16e9 elements
+    pool = torch.empty((slots, 8, 64, 128), dtype=torch.bfloat16, device="cuda")
+    c = WindowCase([(1, 130), (20, 150)], 1 << 20, 0)
+    far = torch.full_like(c.d_table, -1)
+    for b in range(2):
+        for i in range(3):
+            s = int(c.d_table[b, i])
+            far[b, i] = slots - 1 - 3 * b - i
+            pool[slots - 1 - 3 * b - i] = c.d_k[s]
+    want = WindowCase.call(c)
+    c.d_v, c.d_k = c.d_k, c.d_k                    # keys for values: one pool does
+    want = c.call()
+    c.d_table, c.d_k, c.d_v = far, pool, pool
+    assert torch.equal(c.call(), want)
+    out = torch.empty((1, 64, 128), dtype=torch.bfloat16, device="cuda")
+    ws = lsa.new_prefix_attn_workspace(1, 1)
+    lsa.lsa_prefix_decode_attn(c.d_q[:1], pool, pool, far[1:, :2].contiguous(), i32([0, 1]), i32([128]), far[:1], i32([130]),
+                               out, ws)
+    k = torch.cat((c.kv[1][0][:128], c.kv[0][0]))
+    assert_close(out, *attend(c.q[:1], k, k, torch.ones((1, 258), dtype=torch.bool)))
+    qkv = torch.randn((1, 80 * 128), device="cuda").to(torch.bfloat16)
+    write = lambda v: lsa.lsa_qk_norm_rope_pool(qkv, None, None, torch.empty_like(out), pool, v, far[:1], i32([0]),  # noqa: E731
+                                                i32([129]), far.shape[1])
+    with pytest.raises(lsa.LsaError, match="INVALID_ARG"):   # K and V of a token in one place
+        write(pool)
+    values = torch.empty_like(pool)
+    write(values)
+    assert torch.equal(pool[slots - 3, :, 1], qkv.view(80, 128)[64:72])
+    assert torch.equal(values[slots - 3, :, 1], qkv.view(80, 128)[72:])
+    clean()
+
+
+def test_the_largest_batch():
+    B = 4096
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v, q = (torch.randn((B, n, m, 128), generator=g, device="cuda").to(torch.bfloat16) for n, m in ((8, 64), (8, 64), (64, 1)))
+    q = q.view(B, 64, 128)
+    n = torch.randint(0, 65, (B,), generator=g, device="cuda", dtype=torch.int32)
+    out, out2 = torch.empty_like(q), torch.empty_like(q)
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    lsa.lsa_window_attn(q, k, v, None, cu, n, 1, 1, 1 << 20, 0, out, lsa.new_window_attn_workspace(B, 1))
+    # as a prefix call: groups of 1 to 64 sequences without a prefix, own tokens only
+    cut = sorted({0, B} | {int(x) for x in torch.randint(1, B, (200,), generator=torch.Generator().manual_seed(1))})
+    G = len(cut) - 1
+    lsa.lsa_prefix_decode_attn(q, k, v, i32([[0]] * G), i32(cut), i32([0] * G), None, n, out2,
+                               lsa.new_prefix_attn_workspace(B, G), max_chunks=1)
+    for b in list(range(0, B, 257)) + [B - 1]:
+        m = int(n[b])
+        ref = attend(q[b: b + 1].cpu(), k[b, :, :m].transpose(0, 1).cpu(), v[b, :, :m].transpose(0, 1).cpu(),
+                     torch.ones((1, m), dtype=torch.bool))
+        assert_close(out[b: b + 1], *ref)
+        assert_close(out2[b: b + 1], *ref)
+    assert bool((out[n == 0] == 0).all()) and bool((out2[n == 0] == 0).all())
+    clean()
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_nothing_is_written_outside_the_buffers(prefix):
+    """The output and the workspace, exactly as large as asked for, between guards."""
+    c = (PrefixCase([(40, 700), (3, 90)], [(17 * i) % 150 for i in range(50)]) if prefix
+         else WindowCase([(150, 400), (1, 900), (40, 100), (9, 9)], 200, 3))
+    guarded = lambda n: torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")  # noqa: E731
+    n, m = c.ws.numel(), c.d_q.numel() * 2
+    ws, out = guarded(n), guarded(m)
+    ws[4096: 4096 + n] = 0
+    want = c.call()
+    got = c.call(out[4096: 4096 + m].view(torch.bfloat16).view(c.d_q.shape), workspace=ws[4096: 4096 + n])
+    assert torch.equal(got, want)
+    for x, size in ((ws, n), (out, m)):
+        assert bool((x[:4096] == 0xA5).all()) and bool((x[4096 + size:] == 0xA5).all())
+    clean()

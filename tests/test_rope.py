@@ -75,14 +75,15 @@ def dense(L, qkv=0x100000, stride=10240, T=1, wq=None, wk=None, eps=1e-6, pos=0x
     (dict(eps=float("inf")), INVALID), (dict(scale=float("inf")), INVALID), (dict(flags=2), INVALID),
     (dict(rot=12), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(qkv=0x100008), MISALIGNED),
     (dict(stride=10244), MISALIGNED), (dict(q=0x400002), MISALIGNED), (dict(v=0x600008), MISALIGNED),
-    (dict(wq=0x700004), MISALIGNED), (dict(wk=0x700008), MISALIGNED)])
+    (dict(k=0x600000), INVALID), (dict(k=0x400000), INVALID), (dict(v=0x400000), INVALID), (dict(wq=0x700004), MISALIGNED), (dict(wk=0x700008), MISALIGNED)])
 def test_dense_form_refuses(L, bad, status):
     assert dense(L, **bad) == status
 
 
 @pytest.mark.parametrize("bad,status", [
     (dict(v=None), INVALID), (dict(seq=None), INVALID), (dict(cpos=None), INVALID), (dict(B=0), INVALID),
-    (dict(max_chunks=0), INVALID), (dict(n_slots=0), INVALID), (dict(T=0), INVALID), (dict(v=0x600008), MISALIGNED)])
+    (dict(max_chunks=0), INVALID), (dict(n_slots=0), INVALID), (dict(T=0), INVALID), (dict(v=0x500000), INVALID),
+    (dict(v=0x600008), MISALIGNED)])
 def test_pool_form_refuses(L, bad, status):
     a = dict(v=0x600000, seq=0x700000, cpos=0x200000, B=1, max_chunks=4, n_slots=4, T=1)
     a.update(bad)
