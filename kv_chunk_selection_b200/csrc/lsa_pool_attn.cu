@@ -96,9 +96,10 @@ enum Mode { kWindowNarrow, kWindow, kPrefixes };
 
 // Partials.  A share can hold the end, or a middle, of a tile that began in an
 // earlier one, and the start of a tile that goes on in the next: share c has a
-// slot for each, 2c and 2c + 1, of as many rows as its kind of tile has.  In prefix mode the rows of a whole tile have places of their own,
-// 64 per sequence for its prefix and 64 for its own tokens, since a sequence's
-// output joins both.  Place says how a query's rows lie there.
+// slot for each, 2c and 2c + 1, of as many rows as its kind of tile has.  In
+// prefix mode the rows of a whole tile have places of their own, 64 per sequence
+// for its prefix and 64 for its own tokens, since a sequence's output joins both.
+// Place says how a query's rows lie there.
 struct Work {
   float* o;          // 128 values a row, normalised: the places, the wide slots, the narrow slots
   float* lse;        // [rows], base 2
@@ -113,8 +114,9 @@ struct Work {
                      // prefix, of the own tokens
   int* ok;           // prefix mode: the offsets were valid
 };
-// The first partial of a (sequence, KV head): its share, whether of the wide list, the query's block and number there, or that the rows are
-// in their own place; kNone: no partial.
+// The first partial of a (sequence, KV head): its share, whether of the wide
+// list, the query's block and number there, or that the rows are in their own
+// place; kNone: no partial.
 constexpr int kEndShare = 0x3ff, kEndWide = 1 << 11, kEndPlace = 16, kEndWhole = 1 << 24, kNone = -1;
 
 // The queries and the keys of one list entry: a sequence, or a group over its prefix.
@@ -790,7 +792,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   for (int v = v_lo; v < v_hi; ++v) {
     s_last = load_list<kPrefix>(plan, v);
     if (s_last.len < 0 && blockIdx.x == 0) set_status(status, LSA_DEV_ERR_BAD_COUNT);
-    bad |= s_last.nq < 0 || s_last.nq > plan.max_q;
+    // (Each entry's rows by themselves: offsets may wrap around and still end in range.)
+    bad |= s_last.nq < 0 || s_last.nq > plan.max_q || s_last.q0 < 0 || s_last.q0 > plan.rows - s_last.nq;
     mine[0] += span<kPrefix>(plan, s_last, false);
     if (kHasWide) mine[1] += span<kPrefix>(plan, s_last, true);
   }
@@ -801,11 +804,11 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   block_scan<kThreads / 32, kHasWide ? 2 : 1>(mine, before, total, scan);
   const Partition part_n(total[0], 2 * gridDim.x), part_w(total[1], gridDim.x);
   if (part_n.base >= (1 << 30) || part_w.base >= (1 << 30)) bad = 1;   // a share counts its units in 32 bits
+  if (bad && blockIdx.x == 0 && tid == 0) set_status(status, LSA_DEV_ERR_CAPACITY);
   if (sm & 1023u) {                      // the 128-byte swizzle repeats every 1024 bytes
     if (tid == 0) set_status(status, LSA_DEV_ERR_INTERNAL);
     bad = 1;
   }
-  if (bad && blockIdx.x == 0 && tid == 0) set_status(status, LSA_DEV_ERR_CAPACITY);
   const int me = blockIdx.x;
   // Prefix mode: sequences from `grouped` on belong to no group.
   const int grouped = plan.groups ? ld_dep(plan.cu + plan.groups) : 0;

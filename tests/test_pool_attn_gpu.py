@@ -209,6 +209,22 @@ def test_prefix_identity_layout_repeats_and_captures():
     clean()
 
 
+def test_offsets_that_wrap_around():
+    """Steps of 2^30 with max_q as large: every difference is in range and the last offset is too, but not the rows."""
+    c = WindowCase([(1, 5)] * 4 + [(4, 9)], 8, 0)
+    good = c.call()
+    cu, c.max_q = c.d_cu, 1 << 30
+    c.d_cu = i32([0, 1 << 30, -(1 << 31), -(1 << 30), 0, 8])
+    ws = lsa.new_window_attn_workspace(5, 1 << 30)
+    out = c.call(workspace=ws)
+    assert lsa.read_device_status() == CAPACITY and bool((out == 3.0).all())
+    c.d_cu = cu
+    c.check(c.call(workspace=ws))   # a bound far above the batch's own is allowed
+    c.max_q = 4
+    assert torch.equal(c.call(), good)
+    clean()
+
+
 def test_prefix_refuses_bad_offsets_and_reports_lengths_and_slots():
     c = PrefixCase([(2, 100), (3, 70)], [5, 6, 7, 8, 9, 10])
     ref, mag = c.reference()
