@@ -387,6 +387,17 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// A query's 8 rows of 64 dims to the output, by the async proxy: issued by a lane,
+// whose group it is.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\tcp.async.bulk.commit_group;" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
@@ -728,7 +739,7 @@ template <Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_q16, const __grid_constant__ CUtensorMap tm_q8,
-                 const __grid_constant__ CUtensorMap tm_q1, const Plan plan, const Work work, float scale_log2,
+                 const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_out, const Plan plan, const Work work, float scale_log2,
                  __nv_bfloat16* __restrict__ out, unsigned* status) {
   constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowNarrow, kHasWide = kMode != kWindowNarrow;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -770,6 +781,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     tma_prefetch_desc(&tm_q16);
     tma_prefetch_desc(&tm_q8);
     tma_prefetch_desc(&tm_q1);
+    tma_prefetch_desc(&tm_out);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -1307,17 +1319,15 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const bool whole = sg.flags & kSegWhole, final = whole && (!kPrefix || (sg.flags & kSegAlone));
           const int row0 = sg.row + i_first, head = sg.head;   // the warp's first query, its first query head
           if (final) {
-            // Output rows (query, head), 128 bytes of a row per 8 lanes.  A thread
-            // holds a row, so the rows turn in the warp's 4 KiB of shared memory,
-            // 16-byte piece x of row y at place x ^ (y % 8) (no bank conflicts
-            // either way).
-            uint8_t* const mine = smem + kTurnAt + warp * kTurnBytes;
-            uint8_t* const row_at = mine + lane * 128;
-            const uint8_t* const from = mine + (lane >> 3) * 128;
-            uint8_t* to = reinterpret_cast<uint8_t*>(
-                out + ((static_cast<int64_t>(row0) * kNumQHeads + head + (lane >> 3)) * kHeadDim + (lane & 7) * 8));
+            // Output rows (query, head): 64 dims at a time through the warp's 4 KiB of
+            // shared memory, 16-byte piece x of row y at x ^ (y % 8) (the map's 128-byte
+            // swizzle), and from there by TMA, 8 rows of a query at once.  The next
+            // tile does not wait for them.
+            uint8_t* const row_at = smem + kTurnAt + warp * kTurnBytes + lane * 128;
 #pragma unroll 1
-            for (int c = 0; c < kHeadDim; c += 64, to += 128) {
+            for (int c = 0; c < kHeadDim; c += 64) {
+              stores_read();                         // what lay here before has been read
+              __syncwarp();
 #pragma unroll
               for (int z = 0; z < 8; z += 4) {
                 float o[32];
@@ -1331,13 +1341,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                       make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
                                  pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
               }
+              fence_proxy_async_smem();
               __syncwarp();
-#pragma unroll
-              for (int x = 0; x < 8; ++x)            // rows 4 x + lane / 8: query x / 2
-                if ((x >> 1) < queries)
-                  *reinterpret_cast<uint4*>(to + (x >> 1) * (kNumQHeads * kHeadDim * 2) + (x & 1) * (4 * kHeadDim * 2)) =
-                      *reinterpret_cast<const uint4*>(from + x * 512 + (((lane & 7) ^ (4 * (x & 1) + (lane >> 3))) << 4));
-              __syncwarp();
+              if (lane < queries) store_box(&tm_out, c, head, row0 + lane, sm + kTurnAt + warp * kTurnBytes + lane * 1024);
             }
           } else {
             const Place at_o = whole ? own_place(work, plan.B, row0 + (lane >> 3), head >> 3, !(sg.flags & kSegGroup))
@@ -1400,6 +1406,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       }
       if (share == 0) wide_units = at;
     }
+    stores_done();
   }
   __syncwarp();
   tcgen05_fence_before();
@@ -1559,12 +1566,13 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
       g_attr_set[kMode][dev] = true;
     }
   }
-  CUtensorMap tm_k, tm_v, tm_q16, tm_q8, tm_q1;
+  CUtensorMap tm_k, tm_v, tm_q16, tm_q8, tm_q1, tm_out;
   int st = encode_pool(&tm_k, k_pool, plan.n_slots);
   if (st == LSA_OK) st = encode_pool(&tm_v, v_pool, plan.n_slots);
   if (st == LSA_OK) st = encode_q(&tm_q16, q, plan.rows, kWideQ / 2);
   if (st == LSA_OK) st = encode_q(&tm_q8, q, plan.rows, kNarrowQ);
   if (st == LSA_OK) st = encode_q(&tm_q1, q, plan.rows, 1);
+  if (st == LSA_OK) st = encode_q(&tm_out, out, plan.rows, 1);
   if (st != LSA_OK) return st;
   // As many CTAs as the most that there can be to do is worth, one per SM.
   const int most = sms < kMaxCtas ? sms : kMaxCtas;
@@ -1572,7 +1580,7 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   const int grid = want < most ? static_cast<int>(want) : most;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(out);
-  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, plan, work,
+  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, tm_out, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
     launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work,
