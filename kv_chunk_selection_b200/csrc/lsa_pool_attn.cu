@@ -21,10 +21,9 @@
 // a long window, a ragged batch and a long prompt all fill the chip evenly.  A
 // tile that a cut splits leaves partials (normalised rows and their
 // log-sum-exps), which are folded in the order of the shares, so that the result
-// does not depend on timing: by the share that adds a tile's last one where a
-// window call has narrow tiles only (no second launch), else by a second kernel
-// (the partials of wide tiles are too many for one SM: 32 sequences over a
-// prefix of 32768 tokens leave 19 MB).
+// does not depend on timing: by the share that adds a tile's last one where that
+// is little for one SM (single tokens: no second launch), else by a second kernel
+// (32 sequences over a prefix of 32768 tokens leave 19 MB).
 //
 // A CTA (one per SM, 12 warps) has two pipelines w = 0, 1 of
 //   warps 4w..4w+3  a softmax warpgroup, a thread per row: the scores of a unit
@@ -90,8 +89,9 @@ struct Plan {
   int64_t n_slots;
 };
 // What a launch can meet: a window call whose sequences have at most kNarrowQ
-// queries (narrow tiles only, folded in the kernel), any window call, a prefix
-// call.  Each has only its own code: the softmax loop has no registers to spare.
+// queries (narrow tiles only) and few partials to a tile, which are folded in the
+// kernel; any window call; a prefix call.  Each has only its own code: the softmax
+// loop has no registers to spare.
 enum Mode { kWindowNarrow, kWindow, kPrefixes };
 
 // Partials.  A share can hold the end, or a middle, of a tile that began in an
@@ -1426,16 +1426,17 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // Window mode.  The queries of a split tile are shared out over the slots that
 // hold its partials.  CTA (x, y) for x below 2 grid: slot x of the wide shares, 2
 // warps (half the dims each) to a query, 16 queries of a tile in two parts at
-// once over y; further x: a warp to each slot of the narrow shares.  (A CTA of 8
-// warps per share took 20 us more at 4096 tokens.)
+// once over y (a CTA of 8 warps per share took 20 us more at 4096 tokens);
+// further x: 2 slots of the narrow shares, 4 warps (a quarter of the dims each) to
+// a query, since such a tile can have a partial for every few units.
 constexpr int kMergeWarps = 8, kMergeY = 4;
 __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wide = static_cast<int>(blockIdx.x) < 2 * grid;
-  const int slot = wide ? blockIdx.x : (blockIdx.x - 2 * grid) * kMergeWarps + warp;
-  if (!wide && (blockIdx.y || slot >= 4 * grid)) return;
+  const int slot = wide ? blockIdx.x : (blockIdx.x - 2 * grid) * 2 + (warp >> 2);
+  if (!wide && blockIdx.y) return;
   const uint4 a = ld_dep(reinterpret_cast<const uint4*>(work.parts + (wide ? 0 : 2 * kMaxCtas) + slot));
   if (!a.w) return;
   const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
@@ -1445,8 +1446,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(const Wo
     const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
     const auto at = [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); };
     __nv_bfloat16* const to = out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + static_cast<int>(a.y) * kGroup) * kHeadDim;
-    fold_query<2, 4>(work, n, lane, at, to, wide ? warp & 1 : 0);
-    if (!wide) fold_query<2, 4>(work, n, lane, at, to, 1);
+    if (wide) fold_query<2, 4>(work, n, lane, at, to, warp & 1);
+    else fold_query<4, 12>(work, n, lane, at, to, warp & 3);
   }
 }
 
@@ -1586,7 +1587,7 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
     launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work,
                plan.B, o);
   else if (kMode == kWindow)
-    launch_pdl(true, window_merge_kernel, dim3(2 * grid + (4 * grid + kMergeWarps - 1) / kMergeWarps, kMergeY),
+    launch_pdl(true, window_merge_kernel, dim3(4 * grid, kMergeY),
                dim3(32 * kMergeWarps), 0, s, work, grid, o);
   return launch_status();
 }
@@ -1630,7 +1631,11 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
   const int64_t seen = static_cast<int64_t>(plan.window) / kChunkTokens + 3 + plan.sinks / kChunkTokens + 1;
   const int64_t tiles = T / pool::kWideQ + B;
   const int64_t units = kNumKVHeads * tiles * ((seen < max_chunks ? seen : max_chunks) + pool::kTileCost);
-  return max_q <= pool::kNarrowQ
+  // Partials that one SM folds: max_q for each of a tile's shares, at most 2 x 148 /
+  // 8 B of them.  One kernel (two) takes 14 (19) us for 1 query over 4096 tokens,
+  // 20.4 (19.6) for 4, 29 (20) for 8; 30 (23) for 8 of 2 sequences each; 20 (21) for
+  // 8 of 4 each with a window of 1024, 63 (70) of 64.
+  return max_q <= pool::kNarrowQ && max_q <= 2 * B
              ? pool::launch<pool::kWindowNarrow>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream)
              : pool::launch<pool::kWindow>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
 }

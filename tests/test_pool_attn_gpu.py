@@ -45,6 +45,17 @@ def test_pieces_of_a_prompt(nq, window, sinks):
     clean()
 
 
+@pytest.mark.parametrize("window,sinks", [(1 << 20, 0), (70, 5)])
+@pytest.mark.parametrize("B,nq", [(1, 2), (1, 3), (1, 8), (2, 4), (2, 5), (2, 8), (3, 7), (4, 8)])
+def test_a_few_queries_of_a_few_sequences(B, nq, window, sinks):
+    """Both sides of the choice between a fold in the kernel and a second one."""
+    c = WindowCase([(nq - b % 2, 1500 - 400 * b) for b in range(B)], window, sinks, seed=10 * B + nq, spare_rows=2)
+    a = c.call()
+    c.check(a)
+    assert torch.equal(a, c.call())
+    clean()
+
+
 @pytest.mark.parametrize("window,sinks", [(1 << 20, 0), (256, 4), (1, 0), (1, 1)])
 def test_long_prompt_is_split_over_the_chip(window, sinks):
     c = WindowCase([(700, 700)], window, sinks)
