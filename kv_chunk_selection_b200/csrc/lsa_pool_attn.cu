@@ -10,16 +10,18 @@
 //
 //   out = sum_j softmax_j(scale q . k_j) v_j
 //
-// One kernel and one launch serve both.  The work is two lists of units; a unit
-// is 64 tokens (one chunk) of K and V of one KV head, 32 KiB, against the
-// queries of a tile:
+// One kernel serves both.  The work is two lists of units; a unit is 64 tokens
+// (one chunk) of K and V of one KV head, 32 KiB, against the queries of a tile:
 //   wide tiles    9 to 32 queries (x 8 query heads): prompts, large groups;
 //   narrow tiles  up to 8: single tokens, the tokens behind a shared prefix.
 // The units of a list's tiles are laid end to end (a tile's also count kTileCost
-// more, for its start and its end) and cut into equal contiguous shares: one
-// per CTA for the wide list, two per CTA for the narrow one.  So one token over
-// a long window, a ragged batch and a long prompt all fill the chip evenly.  A
-// tile that a cut splits leaves partials (normalised rows and their
+// more, for its start and its end) and cut into equal contiguous shares: one per
+// CTA for the wide list, two per CTA for the narrow one.  So one token over a long
+// window, a ragged batch and a long prompt all fill the chip evenly.  A call with
+// both gives each list its own CTAs, as many as its units cost (every CTA with a
+// share of both, one after the other: 32 sequences over a prefix of 32768 tokens
+// and up to 1024 of their own took 67 us, now 60; 33 queries over 512 tokens 22.7,
+// now 18.1).  A tile that a cut splits leaves partials (normalised rows and their
 // log-sum-exps), which are folded in the order of the shares, so that the result
 // does not depend on timing: by the share that adds a tile's last one where that
 // is little for one SM (single tokens: no second launch), else by a second kernel
@@ -35,13 +37,13 @@
 //                   of two score buffers, O += P V (128 x 128 x 64) with P from
 //                   TMEM;
 //   warp 10 + w     plans and loads (TMA).
-// First the CTA's wide share: both pipelines use every unit, each with half of
-// the tile's queries; warp 10 streams K and V through all 8 half-stages of 16
-// KiB, warp 11 walks the list a few segments ahead and loads the queries.  Then
-// the narrow shares: each pipeline has its own stream through 4 half-stages, so
-// that one's start of a tile, its latencies and its end run beside the other's
-// units; that carries single tokens at the rate of the memory although 8 of the
-// 128 rows of a product are theirs.
+// In a wide share both pipelines use every unit, each with half of the tile's
+// queries; warp 10 streams K and V through all 8 half-stages of 16 KiB, warp 11
+// walks the list a few segments ahead and loads the queries.  Of the narrow shares
+// each pipeline has one, with its own stream through 4 half-stages, so that one's
+// start of a tile, its latencies and its end run beside the other's units; that
+// carries single tokens at the rate of the memory although 8 of the 128 rows of a
+// product are theirs.
 //
 // TMEM (512 columns): scores 2 pipelines x 2 buffers x 64, accumulators 2 x 128.
 // Rows that no query of a tile sees are zeroed in V's stage before the product,
@@ -72,6 +74,11 @@ constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
 constexpr int kTileCost = 3;                 // 2 to 5 measured alike
 constexpr int kMinShare = 3;                 // smallest share of a list worth a pipeline (or a CTA) of its own: one token
                                              // over 4096 takes 16.6 us with 2, 16.0 with 3, 16.2 with 4, 16.8 with 6
+// What a wide unit costs on a CTA, in narrow ones (two pipelines, each with its own).
+// Shared prefixes, groups x sequences over prefix + own tokens: 24 over 8000 + 100
+// take 26.2 us (1.5: 27.0, 2.3: 26.2), 64 over 8000 + 2000 64 (70, 67), 5 x 26 over
+// 16384 + 512 116 (121, 127); pieces of 30 over a window of 1024 64 (69, 67).
+constexpr float kWideCost = 1.8f;
 constexpr int kFmaEvery = 4;                 // of the pairs of powers of two, one in 4 on the FMA pipe
 constexpr float kRaise = 8.f;                // growth of the maximum (log2) that rescales the accumulator
 constexpr int kSCols = 64, kOCol0 = 256;     // TMEM: S[w][b] at (2 w + b) * 64, O[w] at 256 + 128 w
@@ -224,7 +231,7 @@ struct Partition {
   int parts;
   __device__ Partition(int64_t total, int most) {
     const int64_t worth = quotient(total, kMinShare);
-    parts = static_cast<int>(worth < 1 ? 1 : worth < most ? worth : most);
+    parts = static_cast<int>(worth < 1 || most < 1 ? 1 : worth < most ? worth : most);
     base = quotient(total, parts);
     rem = total - base * parts;
   }
@@ -702,38 +709,28 @@ constexpr int kPFull = kSFull + 32, kODone = kPFull + 32;              // probab
 constexpr int kQFull = kODone + 32, kQEmpty = kQFull + 16;             // [2] query tiles of the wide share
 constexpr int kNFull = kQEmpty + 16, kNEmpty = kNFull + 32;            // [2 pipelines][2] of the narrow ones
 constexpr int kSegFull = kNEmpty + 32, kSegDone = kSegFull + 24 * kAhead;   // [3][kAhead]
-constexpr int kHandOver = kSegDone + 24 * kAhead;                      // [2]: 11's part of the wide share is done, 10's is
-constexpr int kDrain = kHandOver + 16, kMeet = kDrain + 16;            // [2], [2]: a warpgroup's warps
+constexpr int kDrain = kSegDone + 24 * kAhead, kMeet = kDrain + 16;            // [2], [2]: a warpgroup's warps
 constexpr int kTmemAt = kMeet + 16, kAbortAt = kTmemAt + 4, kVerdictAt = kAbortAt + 4;   // (two verdicts)
-// The entry at the start of the wide share and of the two narrow ones.
+constexpr int kGridWAt = kVerdictAt + 8;                               // CTAs of the wide list
+// The entry at the start of the wide share, or of the two narrow ones.
 struct Found {
   List s;
   int64_t r, per_head;       // the place in the entry, the entry's places per KV head
   int v;
 };
-constexpr int kFoundAt = kVerdictAt + 8;
-constexpr int kSmemBytes = kFoundAt + 3 * static_cast<int>(sizeof(Found));
+constexpr int kFoundAt = kGridWAt + 8;
+constexpr int kSmemBytes = kFoundAt + 2 * static_cast<int>(sizeof(Found));
 static_assert(kSmemBytes <= 232448 && sizeof(Seg) % 8 == 0 && kFoundAt % 8 == 0, "shared memory of one CTA");
 
 // The place in the ring of the x-th half (K of unit i: 2 i, V: 2 i + 1) of a
-// share, and the parity of its use.  The wide share goes around all 8; the
-// narrow one of pipeline w around 4w .. 4w + 3, with the wide share's uses before
-// (`base`: their parity, `used`: whether there were any, a bit per half).
+// share, and the parity of its use.  A wide share goes around all 8, the narrow
+// one of pipeline w around 4w .. 4w + 3.
 struct Ring {
-  unsigned first, mask, shift, base, used;
+  unsigned first, mask, shift;
   __device__ unsigned half(unsigned x) const { return first + (x & mask); }
-  __device__ unsigned parity(unsigned x) const { return ((x >> shift) ^ (base >> half(x))) & 1; }
+  __device__ unsigned parity(unsigned x) const { return (x >> shift) & 1; }
 };
-__device__ __forceinline__ Ring wide_ring() { return {0, 7, 3, 0, 0}; }
-__device__ __forceinline__ Ring narrow_ring(int w, unsigned wide_units) {
-  unsigned base = 0, used = 0;
-  for (unsigned h = 0; h < kHalves; ++h) {
-    const unsigned uses = (2 * wide_units + 7 - h) >> 3;
-    base |= (uses & 1) << h;
-    used |= (uses ? 1u : 0u) << h;
-  }
-  return {4u * w, 3, 2, base, used};
-}
+__device__ __forceinline__ Ring ring_of(bool wide, int w) { return wide ? Ring{0, 7, 3} : Ring{4u * w, 3, 2}; }
 
 template <Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -743,7 +740,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                  __nv_bfloat16* __restrict__ out, unsigned* status) {
   constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowNarrow, kHasWide = kMode != kWindowNarrow;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (The warp's index by a shuffle: the compiler has to know that it is the same in
+  // every lane, or the products' operands are moved to uniform registers one by one.)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t sm = smem_u32(smem);
   const uint32_t abort_flag = sm + kAbortAt;
 
@@ -763,7 +762,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     for (int i = 0; i < 2; ++i) {
       bar_init(sm + kQFull + 8 * i, 1);
       bar_init(sm + kQEmpty + 8 * i, 1);
-      bar_init(sm + kHandOver + 8 * i, 1);
       bar_init(sm + kDrain + 8 * i, 1);
       bar_init(sm + kMeet + 8 * i, 4);
     }
@@ -812,9 +810,20 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   bad = __syncthreads_or(bad);
   if (bad) mine[0] = mine[1] = 0;
   int64_t total[2] = {0, 0};
-  int64_t before[2];
+  int64_t before[2] = {0, 0};
   block_scan<kThreads / 32, kHasWide ? 2 : 1>(mine, before, total, scan);
-  const Partition part_n(total[0], 2 * gridDim.x), part_w(total[1], gridDim.x);
+  // CTAs of the wide list, the others are the narrow one's: by what the lists cost,
+  // or as many as the shorter one is worth.
+  const int grid = gridDim.x;
+  int grid_w = kHasWide && total[1] ? grid : 0;
+  if (grid_w && total[0]) {
+    const float cost = kWideCost * static_cast<float>(total[1]);
+    grid_w = min(max(static_cast<int>(grid * (cost / (cost + static_cast<float>(total[0]))) + 0.5f), 1), grid - 1);
+    const int64_t worth_w = quotient(total[1], kMinShare), worth_n = (quotient(total[0], kMinShare) + 1) / 2;
+    if (worth_w < grid_w) grid_w = max(static_cast<int>(worth_w), 1);
+    else if (worth_n < grid - grid_w) grid_w = grid - max(static_cast<int>(worth_n), 1);
+  }
+  const Partition part_n(total[0], 2 * (grid - grid_w)), part_w(total[1], grid_w);
   if (part_n.base >= (1 << 30) || part_w.base >= (1 << 30)) bad = 1;   // a share counts its units in 32 bits
   if (bad && blockIdx.x == 0 && tid == 0) set_status(status, LSA_DEV_ERR_CAPACITY);
   if (sm & 1023u) {                      // the 128-byte swizzle repeats every 1024 bytes
@@ -826,11 +835,11 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const int grouped = plan.groups ? ld_dep(plan.cu + plan.groups) : 0;
   if (kPrefix && me == 0 && tid == 0) *work.ok = bad ? 0 : 1;
 #pragma unroll
-  for (int x = kHasWide ? 0 : 1; x < 3; ++x) {   // the entries at the starts of the wide share and of the two narrow ones
-    const int k = x == 0;
-    const int64_t u = x == 0 ? part_w.start(me) : part_n.start(2 * me + x - 1);
-    if (!bad && before[k] <= u && u < before[k] + mine[k]) {   // one thread, if u is in the list
-      int64_t at = before[k], n = mine[k];
+  for (int x = 0; x < 2; ++x) {   // the entry at the start of the wide share, or the entries of the two narrow ones
+    const bool k = me < grid_w;
+    const int64_t u = k ? part_w.start(me) : part_n.start(2 * (me - grid_w) + x);
+    int64_t at = k ? before[1] : before[0], n = k ? mine[1] : mine[0];
+    if (!bad && !(k && x) && at <= u && u < at + n) {   // one thread, if u is in the list
       int v = v_lo;
       List s = s_last;
       if (per > 1) {
@@ -844,6 +853,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       found[x] = {s, u - at, n / kNumKVHeads, v};
     }
   }
+  if (tid == 0) *reinterpret_cast<volatile int*>(smem + kGridWAt) = grid_w;
+  const bool wide = kHasWide && me < grid_w;   // what the CTA does
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
@@ -877,13 +888,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         cur.end = part.start(share + 1);
         put = 0;
         ended = false;
-        if (kMode == kWindow && lane == 0) {
-          int4* const parts = work.parts + (x == 0 ? 0 : 2 * kMaxCtas) + 2 * share;
-          parts[0] = parts[1] = make_int4(0, 0, 0, 0);
-        }
         more = !bad && u < cur.end && u < all;
         if (more) {
-          const Found& f = found[x];
+          const Found& f = found[x == 0 ? 0 : x - 1];
           cur.start(plan, x == 0, f.v, f.s, f.per_head, f.r, u, lane);
           more = cur.units() > 0;
         }
@@ -897,7 +904,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           if (lane == 0) s->units = 0;
           ended = true;
         } else {
-          const bool wide = x == 0, own = kPrefix && cur.v >= plan.groups;
+          const bool own = kPrefix && cur.v >= plan.groups;
           const int units = cur.units();
           const bool begins = cur.j == 0, ends = cur.j + units == cur.n;
           const int flags = (cur.empty ? kSegEmpty : 0) | (cur.tiles > 1 ? kSegAgain : 0) |
@@ -947,7 +954,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       };
       auto advance = [&](int x, const Partition& part, int share) {
         if (more) {
-          const bool wide = x == 0;
           if (kMode == kWindow) {   // what the merge has to know
             const bool begins = cur.j == 0, ends = cur.j + cur.units() == cur.n;
             if (!(begins && ends)) {
@@ -963,13 +969,22 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       };
       const uint64_t policy_once = l2_policy_evict_first(), policy_again = l2_policy_evict_normal();
       const int beyond = static_cast<int>(plan.n_slots) * (kNumKVHeads * kChunkTokens);   // reads as zeros
-      // K and V of a segment's units, which are units x .. of the share.
-      auto load_units = [&](const Ring& ring, unsigned x, int units, int flags, int j0, int first, int low, int g,
-                            const int32_t* table, int64_t ident) {
+      // The narrow shares are 2 turned and the next; every CTA has an index of that
+      // kind too, so that each place of work.parts is written by one lane.
+      const int turned = me - grid_w + (me < grid_w ? grid : 0);
+      if (kMode == kWindow && lane == 0) {
+        int4* const narrow = work.parts + 2 * kMaxCtas + 2 * (2 * turned + w);
+        narrow[0] = narrow[1] = make_int4(0, 0, 0, 0);
+        if (w) work.parts[2 * me] = work.parts[2 * me + 1] = make_int4(0, 0, 0, 0);
+      }
+      const Ring ring = ring_of(wide, w);
+      unsigned halves = 0;   // loads so far
+      // K and V of a segment's units, the next ones of the share.
+      auto load_units = [&](int units, int flags, int j0, int first, int low, int g, const int32_t* table, int64_t ident) {
         // Another tile of the entry reads the same chunks: they stay in L2.
         const uint64_t policy = (flags & kSegAgain) ? policy_again : policy_once;
         int row = 0;
-        for (int i = 0; i < units; ++i, ++x) {
+        for (int i = 0; i < units; ++i) {
           if ((i & 31) == 0) {   // the rows of 32 units at a time, a lane each
             row = beyond;
             if (!(flags & kSegEmpty) && i + lane < units) {
@@ -984,9 +999,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const int y = __shfl_sync(0xffffffffu, row, i & 31);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const unsigned h = ring.half(2 * x + kv);
-            // The use before this one has been read (a half's first use needs no wait).
-            if ((2 * x + kv > ring.mask || ((ring.used >> h) & 1)) && !wait(kEmpty + 8 * h, ring.parity(2 * x + kv) ^ 1)) return false;
+            const unsigned h = ring.half(halves);
+            // The use before this one has been read.
+            if (halves > ring.mask && !wait(kEmpty + 8 * h, ring.parity(halves) ^ 1)) return false;
             if (lane == 0) {
               const uint32_t dst = sm + h * kHalfBytes, bar = sm + kFull + 8 * h;
               const CUtensorMap* const map = kv ? &tm_v : &tm_k;
@@ -997,15 +1012,23 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             __syncwarp();
             // A wide share's first K comes alone: every CTA starts at once, and with
             // the whole ring asked for together the first products would wait 4 us.
-            if (ring.mask == 7 && x == 0 && kv == 0 && !wait(kFull + 8 * h, 0)) return false;
+            if (wide && halves == 0 && !wait(kFull + 8 * h, 0)) {
+              halves = 1;
+              return false;
+            }
+            ++halves;
           }
         }
         return true;
       };
+      // The loads of a share that was given up land before the CTA ends.
+      auto land = [&]() {
+        volatile int never = 0;
+        for (unsigned i = halves > ring.mask ? halves - ring.mask - 1 : 0; i < halves; ++i)
+          mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kFull) + ring.half(i), ring.parity(i), &never);
+      };
       bool ok = true;
-      unsigned wide_units = 0;
-      if (!kHasWide) {
-      } else if (warp == kLoadWarp) {
+      if (wide && warp == kLoadWarp) {
         for (unsigned k = 0; ok; ++k) {
           ok = seg_get(0, k);
           if (!ok) break;
@@ -1015,12 +1038,10 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const int64_t ident = s.ident;
           seg_done(0, k);
           if (units == 0) break;
-          ok = load_units(wide_ring(), wide_units, units, flags, j0, first, low, g, table, ident);
-          wide_units += units;
+          ok = load_units(units, flags, j0, first, low, g, table, ident);
         }
-        if (ok && lane == 0) bar_arrive(sm + kHandOver + 8);
-        if (ok) ok = wait(kHandOver, 0);
-      } else {
+        if (!ok && lane == 0) land();
+      } else if (wide) {
         begin(0, part_w, total[1], me);
         // One place stays free: in segment k the planner writes segment k + 3
         // where k - 1 was, which does not hold back the query tiles of k + 1.
@@ -1030,7 +1051,6 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const Seg& s = segs[k % kAhead];
           const int units = s.units, cnt = s.cnt, row = s.row, head = s.head;
           if (units == 0) break;
-          wide_units += units;
           for (int t = 0; ok && t < 2; ++t) {   // a pipeline's half of the queries each
             if (k) ok = wait(kQEmpty + 8 * t, (k - 1) & 1);
             if (ok && lane == 0) {
@@ -1047,51 +1067,42 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             ok = publish(0, part_w, me);
           }
         }
-        for (int t = 0; ok && k && t < 2; ++t) ok = wait(kQEmpty + 8 * t, (k - 1) & 1);
-        if (ok && lane == 0) bar_arrive(sm + kHandOver);
-        if (ok) ok = wait(kHandOver + 8, 0);
         if (!ok && lane == 0 && k) {   // tiles in flight land before the CTA ends
           volatile int never = 0;
           for (int t = 0; t < 2; ++t)
             mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kQFull) + t, (k - 1) & 1, &never);
         }
-      }
-      // The pipeline's narrow share.
-      const Ring ring = narrow_ring(w, wide_units);
-      unsigned x = 0, loads = 0;
-      if (ok) begin(1 + w, part_n, total[0], 2 * me + w);
-      for (unsigned k = 0; ok; ++k) {
-        const int units = more ? cur.units() : 0, cnt = cur.cnt, row = cur.row(false), j0 = cur.j, first = cur.first,
-                  low = cur.low, g = cur.g, flags = cur.empty ? kSegEmpty : 0;
-        const int32_t* const table = cur.s.table;
-        const int64_t ident = cur.s.ident;
-        ok = publish(1 + w, part_n, 2 * me + w);
-        if (!ok || units == 0) break;
-        const int b = k & 1;
-        if (k >= 2) ok = wait(kNEmpty + 16 * w + 8 * b, ((k >> 1) - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          const uint32_t bar = sm + kNFull + 16 * w + 8 * b, q = sm + kQAt + w * kQTileBytes + b * kQ2Bytes;
-          const CUtensorMap* const map = cnt == 1 ? &tm_q1 : &tm_q8;   // what other rows hold is not read back
-          bar_expect(bar, 2 * 128 * kGroup * (cnt == 1 ? 1 : kNarrowQ));
-          load_box(q, map, 0, g * kGroup, row, bar);
-          load_box(q + kQBoxBytes, map, 64, g * kGroup, row, bar);
+      } else {
+        unsigned loads = 0;
+        begin(1 + w, part_n, total[0], 2 * turned + w);
+        for (unsigned k = 0; ok; ++k) {
+          const int units = more ? cur.units() : 0, cnt = cur.cnt, row = cur.row(false), j0 = cur.j, first = cur.first,
+                    low = cur.low, g = cur.g, flags = cur.empty ? kSegEmpty : 0;
+          const int32_t* const table = cur.s.table;
+          const int64_t ident = cur.s.ident;
+          ok = publish(1 + w, part_n, 2 * turned + w);
+          if (!ok || units == 0) break;
+          const int b = k & 1;
+          if (k >= 2) ok = wait(kNEmpty + 16 * w + 8 * b, ((k >> 1) - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bar = sm + kNFull + 16 * w + 8 * b, q = sm + kQAt + w * kQTileBytes + b * kQ2Bytes;
+            const CUtensorMap* const map = cnt == 1 ? &tm_q1 : &tm_q8;   // what other rows hold is not read back
+            bar_expect(bar, 2 * 128 * kGroup * (cnt == 1 ? 1 : kNarrowQ));
+            load_box(q, map, 0, g * kGroup, row, bar);
+            load_box(q + kQBoxBytes, map, 64, g * kGroup, row, bar);
+          }
+          __syncwarp();
+          ++loads;
+          ok = load_units(units, flags, j0, first, low, g, table, ident);
+          advance(1 + w, part_n, 2 * turned + w);
         }
-        __syncwarp();
-        ++loads;
-        ok = load_units(ring, x, units, flags, j0, first, low, g, table, ident);
-        x += units;
-        advance(1 + w, part_n, 2 * me + w);
-      }
-      if (!ok && lane == 0) {   // copies in flight land before the CTA ends
-        volatile int never = 0;
-        uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kBarAt);
-        for (unsigned i = loads > 2 ? loads - 2 : 0; i < loads; ++i)
-          mbar_wait_bounded(bars + (kNFull - kBarAt) / 8 + 2 * w + (i & 1), (i >> 1) & 1, &never);
-        const unsigned end = 2 * (loads ? x : wide_units);
-        const Ring r = loads ? ring : wide_ring();
-        for (unsigned i = end > r.mask ? end - r.mask - 1 : 0; i < end; ++i)
-          if (loads || warp == kLoadWarp) mbar_wait_bounded(bars + r.half(i), r.parity(i), &never);
+        if (!ok && lane == 0) {   // copies in flight land before the CTA ends
+          volatile int never = 0;
+          uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kNFull) + 2 * w;
+          for (unsigned i = loads > 2 ? loads - 2 : 0; i < loads; ++i) mbar_wait_bounded(bars + (i & 1), (i >> 1) & 1, &never);
+          land();
+        }
       }
     } else {
       // =============================== products ==============================
@@ -1101,62 +1112,57 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       const uint32_t k_lo0 = desc_lo_kmajor(sm), v_lo0 = desc_lo_v(sm), q_lo0 = desc_lo_kmajor(sm + kQAt + w * kQTileBytes);
       const uint32_t o_acc = tmem + kOCol0 + w * kHeadDim, s_col0 = tmem + 2 * w * kSCols;
       const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
-      unsigned job = 0, wide_units = 0;   // units so far, of them in the wide share
+      const Ring ring = ring_of(wide, w);
+      const int x = wide ? 0 : 1 + w;   // the share
+      unsigned job = 0;                 // units so far
       bool ok = true;
-#pragma unroll 1
-      for (int x = kHasWide ? 0 : 1 + w; ok && x <= 1 + w; x += 1 + w) {   // the wide share, then the narrow one
-        const Ring ring = x == 0 ? wide_ring() : narrow_ring(w, wide_units);
-        unsigned at = 0;   // units of the share so far
-        for (unsigned k = 0; ok; ++k) {
-          ok = seg_get(x, k);
-          if (!ok) break;
-          const int n = segs[x * kAhead + k % kAhead].units;
-          seg_done(x, k);
-          if (n == 0) break;
-          const int q_full = x == 0 ? kQFull + 8 * w : kNFull + 16 * w + 8 * (k & 1);
-          const int q_empty = x == 0 ? kQEmpty + 8 * w : kNEmpty + 16 * w + 8 * (k & 1);
-          const uint32_t q_lo = q_lo0 + (x == 0 ? 0 : (k & 1) * (kQ2Bytes >> 4));
-          ok = wait(q_full, (x == 0 ? k : k >> 1) & 1);
-          // Scores run up to two units (both buffers) before the products: in the
-          // narrow share as far as units have arrived, since waiting for one that
-          // has not would hold back the product that frees a half-stage.
-          int next = 0;
-          for (int i = 0; ok && i < n; ++i) {
-            for (; next < min(n, i + 2); ++next) {
-              const unsigned kx = 2 * (at + next), h = ring.half(kx), jb = job + next, buf = jb & 1;
-              if (x && next > i && !__all_sync(0xffffffffu, bar_test(sm + kFull + 8 * h, ring.parity(kx)))) break;
-              // K is there, and the buffer's probabilities have been read.
-              ok = jb < 2 ? wait(kFull + 8 * h, ring.parity(kx))
-                          : wait2(kFull + 8 * h, ring.parity(kx), o_bar + 8 * buf, ((jb - 2) >> 1) & 1);
-              if (!ok) break;
-              tcgen05_fence_after();
-              const uint32_t k_lo = k_lo0 + h * (kHalfBytes >> 4), d = s_col0 + buf * kSCols;
-#pragma unroll
-              for (int y = 0; y < 8; ++y)
-                mma_ss(leader, d, q_lo + (y >> 2) * (kQBoxBytes >> 4) + (y & 3) * 2,
-                       k_lo + (y >> 2) * (kBoxBytes >> 4) + (y & 3) * 2, kIdescS, y > 0);
-              mma_commit(leader, sm + s_bar + 8 * buf);
-              mma_commit(leader, sm + kEmpty + 8 * h);
-              if (x) mma_commit(leader, sm + kEmpty + 8 * h);
-              if (next == n - 1) mma_commit(leader, sm + q_empty);
-            }
-            if (!ok) break;
-            const unsigned vx = 2 * (at + i) + 1, h = ring.half(vx), jb = job + i, buf = jb & 1;
-            ok = wait2(kFull + 8 * h, ring.parity(vx), p_bar + 8 * buf, (jb >> 1) & 1);
+      for (unsigned k = 0; ok; ++k) {
+        ok = seg_get(x, k);
+        if (!ok) break;
+        const int n = segs[x * kAhead + k % kAhead].units;
+        seg_done(x, k);
+        if (n == 0) break;
+        const int q_full = x == 0 ? kQFull + 8 * w : kNFull + 16 * w + 8 * (k & 1);
+        const int q_empty = x == 0 ? kQEmpty + 8 * w : kNEmpty + 16 * w + 8 * (k & 1);
+        const uint32_t q_lo = q_lo0 + (x == 0 ? 0 : (k & 1) * (kQ2Bytes >> 4));
+        ok = wait(q_full, (x == 0 ? k : k >> 1) & 1);
+        // Scores run up to two units (both buffers) before the products: in the
+        // narrow share as far as units have arrived, since waiting for one that
+        // has not would hold back the product that frees a half-stage.
+        int next = 0;
+        for (int i = 0; ok && i < n; ++i) {
+          for (; next < min(n, i + 2); ++next) {
+            const unsigned kx = 2 * (job + next), h = ring.half(kx), jb = job + next, buf = jb & 1;
+            if (x && next > i && !__all_sync(0xffffffffu, bar_test(sm + kFull + 8 * h, ring.parity(kx)))) break;
+            // K is there, and the buffer's probabilities have been read.
+            ok = jb < 2 ? wait(kFull + 8 * h, ring.parity(kx))
+                        : wait2(kFull + 8 * h, ring.parity(kx), o_bar + 8 * buf, ((jb - 2) >> 1) & 1);
             if (!ok) break;
             tcgen05_fence_after();
-            const uint32_t v_lo = v_lo0 + h * (kHalfBytes >> 4), a = s_col0 + buf * kSCols;
+            const uint32_t k_lo = k_lo0 + h * (kHalfBytes >> 4), d = s_col0 + buf * kSCols;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              mma_ts(leader, o_acc, a + 8 * y, v_lo + y * (2048 >> 4), kIdescO, y > 0 || i > 0);
-            mma_commit(leader, sm + o_bar + 8 * buf);
+            for (int y = 0; y < 8; ++y)
+              mma_ss(leader, d, q_lo + (y >> 2) * (kQBoxBytes >> 4) + (y & 3) * 2,
+                     k_lo + (y >> 2) * (kBoxBytes >> 4) + (y & 3) * 2, kIdescS, y > 0);
+            mma_commit(leader, sm + s_bar + 8 * buf);
             mma_commit(leader, sm + kEmpty + 8 * h);
             if (x) mma_commit(leader, sm + kEmpty + 8 * h);
+            if (next == n - 1) mma_commit(leader, sm + q_empty);
           }
-          job += n;
-          at += n;
+          if (!ok) break;
+          const unsigned vx = 2 * (job + i) + 1, h = ring.half(vx), jb = job + i, buf = jb & 1;
+          ok = wait2(kFull + 8 * h, ring.parity(vx), p_bar + 8 * buf, (jb >> 1) & 1);
+          if (!ok) break;
+          tcgen05_fence_after();
+          const uint32_t v_lo = v_lo0 + h * (kHalfBytes >> 4), a = s_col0 + buf * kSCols;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mma_ts(leader, o_acc, a + 8 * y, v_lo + y * (2048 >> 4), kIdescO, y > 0 || i > 0);
+          mma_commit(leader, sm + o_bar + 8 * buf);
+          mma_commit(leader, sm + kEmpty + 8 * h);
+          if (x) mma_commit(leader, sm + kEmpty + 8 * h);
         }
-        if (x == 0) wide_units = at;
+        job += n;
       }
       mma_commit(leader, sm + kDrain + 8 * w);   // every product has ended before TMEM is given back
       volatile int never = 0;
@@ -1170,7 +1176,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t s_col0 = tmem + 2 * w * kSCols + lanes, o_col0 = tmem + kOCol0 + w * kHeadDim + lanes;
     const int s_bar = kSFull + 16 * w, p_bar = kPFull + 16 * w, o_bar = kODone + 16 * w;
     const uint64_t scale2 = pack2(scale_log2, scale_log2);
-    unsigned job = 0, wide_units = 0, meets = 0;
+    const int share = wide ? 0 : 1 + w;
+    unsigned job = 0, meets = 0;      // units so far
     bool ok = true;
     // The warps of the warpgroup.
     auto meet = [&]() {
@@ -1178,233 +1185,226 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (lane == 0) bar_arrive(sm + kMeet + 8 * w);
       return wait(kMeet + 8 * w, meets++ & 1);
     };
+    for (unsigned k = 0; ok; ++k) {
+      ok = seg_get(share, k);
+      if (!ok) break;
+      const Seg& sg = segs[share * kAhead + k % kAhead];
+      const int n = sg.units, j0 = sg.j0, f0 = sg.f0 - j0, f1 = sg.f1 - j0, f2 = sg.f2 - j0;
+      if (n == 0) break;
+      // The warp's queries: i_first .. of the tile, 4 at most.
+      const int half = (sg.cnt + 1) >> 1;
+      const int i_first = (wide && w ? half : 0) + 4 * wq;
+      const int queries = min(4, (wide && !w ? half : sg.cnt) - i_first);
+      float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int share = kHasWide ? 0 : 1 + w; ok && share <= 1 + w; share += 1 + w) {
-      const bool wide = share == 0;
-      unsigned at = 0;
-      for (unsigned k = 0; ok; ++k) {
-        ok = seg_get(share, k);
-        if (!ok) break;
-        const Seg& sg = segs[share * kAhead + k % kAhead];
-        const int n = sg.units, j0 = sg.j0, f0 = sg.f0 - j0, f1 = sg.f1 - j0, f2 = sg.f2 - j0;
-        if (n == 0) break;
-        // The warp's queries: i_first .. of the tile, 4 at most.
-        const int half = (sg.cnt + 1) >> 1;
-        const int i_first = (wide && w ? half : 0) + 4 * wq;
-        const int queries = min(4, (wide && !w ? half : sg.cnt) - i_first);
-        float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          const unsigned buf = (job + i) & 1;
-          uint64_t see = ~0ull;                      // tokens of the unit that this row sees
-          const bool edge = !(i < f0 || (i >= f1 && i <= f2));
-          ok = wait(s_bar + 8 * buf, ((job + i) >> 1) & 1);
-          if (!ok) break;
-          tcgen05_fence_after();
-          if (edge) {
-            uint64_t any;                            // tokens that some query of the tile sees
-            const int j = j0 + i, kb = (j < sg.first ? j : sg.low + j - sg.first) * kChunkTokens;
-            if (sg.flags & kSegEmpty) {
-              any = see = 0;
-            } else if (kPrefix) {
-              any = see = lowest(sg.len - kb);
-            } else {
-              const int pos = sg.p0 + i_first + (lane >> 3) - kb;   // of the row's query, in the unit
-              any = lowest(sg.p0 + sg.cnt - kb) & (~lowest(sg.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
-              see = lowest(pos + 1) & (~lowest(pos - plan.window + 1) | lowest(plan.sinks - kb));
-            }
-            if (any != ~0ull) {
-              // Unseen rows of V become zeros (their probabilities are zero, what
-              // the page holds there may not be finite).  Both pipelines write the
-              // same zeros to a wide tile's.
-              const Ring ring = wide ? wide_ring() : narrow_ring(w, wide_units);
-              const unsigned vx = 2 * (at + i) + 1, h = ring.half(vx);
-              ok = wait(kFull + 8 * h, ring.parity(vx));
-              if (!ok) break;
-              uint8_t* const vs = smem + h * kHalfBytes;
-              for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
-                const int row = x >> 4;
-                if (!((any >> row) & 1))
-                  *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-            }
-          }
-          if (queries > 0) {
-            const uint32_t sp = s_col0 + buf * kSCols;
-            float s[64];
-            tmem_ld32(sp, s);
-            tmem_ld32(sp + 32, s + 32);
-            tmem_wait_ld(s, 64);
-            if (edge) {
-              const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                if (!((see0 >> c) & 1)) s[c] = -INFINITY;
-                if (!((see1 >> c) & 1)) s[c + 32] = -INFINITY;
-              }
-            }
-            float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
-#pragma unroll
-            for (int c = 12; c < 60; c += 8) {
-              mx[0] = max3(mx[0], s[c], s[c + 1]);
-              mx[1] = max3(mx[1], s[c + 2], s[c + 3]);
-              mx[2] = max3(mx[2], s[c + 4], s[c + 5]);
-              mx[3] = max3(mx[3], s[c + 6], s[c + 7]);
-            }
-            mx[0] = max3(mx[0], s[60], s[61]);
-            mx[1] = max3(mx[1], s[62], s[63]);
-            const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
-            const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;   // a row's first score that is not masked always does
-            if (__any_sync(0xffffffffu, raise)) {
-              const float m_new = raise ? top : m;
-              const float f = raise ? fast_exp2(m - m_new) : 1.f;
-              m = m_new;
-              l *= f;
-              if (i > 0) {                           // the accumulator of earlier units follows
-                ok = wait(o_bar + 8 * (buf ^ 1), ((job + i - 1) >> 1) & 1);
-                if (!ok) break;
-                tcgen05_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < kHeadDim; c += 32) {
-                  float o[32];
-                  tmem_ld32(o_col0 + c, o);
-                  tmem_wait_ld(o, 32);
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) o[x] *= f;
-                  tmem_st32(o_col0 + c, o);
-                }
-              }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every probability is 0
-            const uint64_t ref2 = pack2(-ref, -ref);
-            uint64_t sum[4] = {0, 0, 0, 0};
-            float pk[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float a, b;
-              const uint64_t x = fma2(pack2(s[2 * c], s[2 * c + 1]), scale2, ref2);
-              if (c % kFmaEvery == kFmaEvery - 1) {
-                exp2_fma(x, a, b);
-              } else {
-                unpack2(x, a, b);
-                a = fast_exp2(a);
-                b = fast_exp2(b);
-              }
-              sum[c & 3] = add2(sum[c & 3], pack2(a, b));
-              // One rounding of the probabilities to bf16, half a step (2^-9) at
-              // most: the output is rounded to the same type.
-              pk[c] = __uint_as_float(pack_bf16(a, b));
-            }
-            tmem_st32(sp, pk);
-            float sa, sb;
-            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), sa, sb);
-            l += sa + sb;
-            tmem_wait_st();
-          }
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(sm + p_bar + 8 * buf);
-        }
-        if (!ok) break;
-
-        // ---- the end of a segment: the output of a whole tile, or a partial ----
-        job += n;
-        at += n;
-        ok = wait(o_bar + 8 * ((job - 1) & 1), ((job - 1) >> 1) & 1);   // its commit follows all earlier products
+      for (int i = 0; i < n; ++i) {
+        const unsigned buf = (job + i) & 1;
+        uint64_t see = ~0ull;                      // tokens of the unit that this row sees
+        const bool edge = !(i < f0 || (i >= f1 && i <= f2));
+        ok = wait(s_bar + 8 * buf, ((job + i) >> 1) & 1);
         if (!ok) break;
         tcgen05_fence_after();
+        if (edge) {
+          uint64_t any;                            // tokens that some query of the tile sees
+          const int j = j0 + i, kb = (j < sg.first ? j : sg.low + j - sg.first) * kChunkTokens;
+          if (sg.flags & kSegEmpty) {
+            any = see = 0;
+          } else if (kPrefix) {
+            any = see = lowest(sg.len - kb);
+          } else {
+            const int pos = sg.p0 + i_first + (lane >> 3) - kb;   // of the row's query, in the unit
+            any = lowest(sg.p0 + sg.cnt - kb) & (~lowest(sg.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
+            see = lowest(pos + 1) & (~lowest(pos - plan.window + 1) | lowest(plan.sinks - kb));
+          }
+          if (any != ~0ull) {
+            // Unseen rows of V become zeros (their probabilities are zero, what
+            // the page holds there may not be finite).  Both pipelines write the
+            // same zeros to a wide tile's.
+            const Ring ring = ring_of(wide, w);
+            const unsigned vx = 2 * (job + i) + 1, h = ring.half(vx);
+            ok = wait(kFull + 8 * h, ring.parity(vx));
+            if (!ok) break;
+            uint8_t* const vs = smem + h * kHalfBytes;
+            for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
+              const int row = x >> 4;
+              if (!((any >> row) & 1))
+                *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
         if (queries > 0) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const bool whole = sg.flags & kSegWhole, final = whole && (!kPrefix || (sg.flags & kSegAlone));
-          const int row0 = sg.row + i_first, head = sg.head;   // the warp's first query, its first query head
-          if (final) {
-            // Output rows (query, head): 64 dims at a time through the warp's 4 KiB of
-            // shared memory, 16-byte piece x of row y at x ^ (y % 8) (the map's 128-byte
-            // swizzle), and from there by TMA, 8 rows of a query at once.  The next
-            // tile does not wait for them.
-            uint8_t* const row_at = smem + kTurnAt + warp * kTurnBytes + lane * 128;
-#pragma unroll 1
-            for (int c = 0; c < kHeadDim; c += 64) {
-              stores_read();                         // what lay here before has been read
-              __syncwarp();
+          const uint32_t sp = s_col0 + buf * kSCols;
+          float s[64];
+          tmem_ld32(sp, s);
+          tmem_ld32(sp + 32, s + 32);
+          tmem_wait_ld(s, 64);
+          if (edge) {
+            const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-              for (int z = 0; z < 8; z += 4) {
+            for (int c = 0; c < 32; ++c) {
+              if (!((see0 >> c) & 1)) s[c] = -INFINITY;
+              if (!((see1 >> c) & 1)) s[c + 32] = -INFINITY;
+            }
+          }
+          float mx[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
+#pragma unroll
+          for (int c = 12; c < 60; c += 8) {
+            mx[0] = max3(mx[0], s[c], s[c + 1]);
+            mx[1] = max3(mx[1], s[c + 2], s[c + 3]);
+            mx[2] = max3(mx[2], s[c + 4], s[c + 5]);
+            mx[3] = max3(mx[3], s[c + 6], s[c + 7]);
+          }
+          mx[0] = max3(mx[0], s[60], s[61]);
+          mx[1] = max3(mx[1], s[62], s[63]);
+          const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
+          const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;   // a row's first score that is not masked always does
+          if (__any_sync(0xffffffffu, raise)) {
+            const float m_new = raise ? top : m;
+            const float f = raise ? fast_exp2(m - m_new) : 1.f;
+            m = m_new;
+            l *= f;
+            if (i > 0) {                           // the accumulator of earlier units follows
+              ok = wait(o_bar + 8 * (buf ^ 1), ((job + i - 1) >> 1) & 1);
+              if (!ok) break;
+              tcgen05_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < kHeadDim; c += 32) {
                 float o[32];
-                tmem_ld32(o_col0 + c + 8 * z, o);
+                tmem_ld32(o_col0 + c, o);
                 tmem_wait_ld(o, 32);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= inv;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
-                      make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                                 pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane < queries) store_box(&tm_out, c, head, row0 + lane, sm + kTurnAt + warp * kTurnBytes + lane * 1024);
-            }
-          } else {
-            const Place at_o = whole ? own_place(work, plan.B, row0 + (lane >> 3), head >> 3, !(sg.flags & kSegGroup))
-                                     : slot_place(work, wide, sg.slot, wide ? warp : wq, lane >> 3);
-            float* const to = work.o + at_o.o + (lane & 7) * 4;
-            const bool valid = (lane >> 3) < queries;
-#pragma unroll 1
-            for (int c = 0; c < kHeadDim; c += 32) {
-              float o[32];
-              tmem_ld32(o_col0 + c, o);
-              tmem_wait_ld(o, 32);
-              if (valid) {
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  *reinterpret_cast<float4*>(to + (c / 4 + x) * at_o.stride) =
-                      make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+                for (int x = 0; x < 32; ++x) o[x] *= f;
+                tmem_st32(o_col0 + c, o);
               }
             }
-            if (valid) work.lse[at_o.lse + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
           }
-          tcgen05_fence_before();
-          if (kPrefix && lane < queries) {   // where the merge finds the partials
-            const int part = (sg.flags & kSegGroup) ? 0 : 2, pairs = plan.B * kNumKVHeads;
-            int* const ends = work.ends + (row0 + lane) * kNumKVHeads + (head >> 3);
-            if (j0 == 0)
-              ends[part * pairs] = final ? kNone
-                                         : (sg.slot >> 1) | (wide ? kEndWide : 0) |
-                                               (((wide ? warp : wq) * 4 + lane) << kEndPlace) | (whole ? kEndWhole : 0);
-            if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.slot >> 1;
-            if (sg.flags & kSegAlone) ends[0] = kNone;
+          const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: every probability is 0
+          const uint64_t ref2 = pack2(-ref, -ref);
+          uint64_t sum[4] = {0, 0, 0, 0};
+          float pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float a, b;
+            const uint64_t x = fma2(pack2(s[2 * c], s[2 * c + 1]), scale2, ref2);
+            if (c % kFmaEvery == kFmaEvery - 1) {
+              exp2_fma(x, a, b);
+            } else {
+              unpack2(x, a, b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+            }
+            sum[c & 3] = add2(sum[c & 3], pack2(a, b));
+            // One rounding of the probabilities to bf16, half a step (2^-9) at
+            // most: the output is rounded to the same type.
+            pk[c] = __uint_as_float(pack_bf16(a, b));
           }
-        }
-        if (kFold && !(sg.flags & kSegWhole)) {
-          // Few queries a sequence: the share that adds a tile's last units folds
-          // its rows, a quarter of the dims a warp.
-          int* const verdict = reinterpret_cast<int*>(smem + kVerdictAt) + w;
-          __threadfence();
-          ok = meet();                               // the partial is written
-          if (!ok) break;
-          if (wq == 0 && lane == 0) {
-            int* const count = work.count + sg.lo;
-            __threadfence();
-            const bool last = atomicAdd(count, n) + n == sg.all;
-            if (last) *count = 0;
-            *verdict = last;
-          }
-          ok = meet();
-          if (!ok) break;
-          if (*verdict) {
-            __threadfence();
-            const int lo = sg.lo, cnt = sg.cnt;
-            for (int i = 0; i < cnt; ++i)
-              fold_query<4, 12>(work, sg.hi - lo + 1, lane,
-                                [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), i >> 2, i & 3); },
-                                out + ((static_cast<int64_t>(sg.row) + i) * kNumQHeads + sg.head) * kHeadDim, wq);
-          }
+          tmem_st32(sp, pk);
+          float sa, sb;
+          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), sa, sb);
+          l += sa + sb;
+          tmem_wait_st();
         }
         tcgen05_fence_before();
-        seg_done(share, k);
+        __syncwarp();
+        if (lane == 0) bar_arrive(sm + p_bar + 8 * buf);
       }
-      if (share == 0) wide_units = at;
+      if (!ok) break;
+
+      // ---- the end of a segment: the output of a whole tile, or a partial ----
+      job += n;
+      ok = wait(o_bar + 8 * ((job - 1) & 1), ((job - 1) >> 1) & 1);   // its commit follows all earlier products
+      if (!ok) break;
+      tcgen05_fence_after();
+      if (queries > 0) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool whole = sg.flags & kSegWhole, final = whole && (!kPrefix || (sg.flags & kSegAlone));
+        const int row0 = sg.row + i_first, head = sg.head;   // the warp's first query, its first query head
+        if (final) {
+          // Output rows (query, head): 64 dims at a time through the warp's 4 KiB of
+          // shared memory, 16-byte piece x of row y at x ^ (y % 8) (the map's 128-byte
+          // swizzle), and from there by TMA, 8 rows of a query at once.  The next
+          // tile does not wait for them.
+          uint8_t* const row_at = smem + kTurnAt + warp * kTurnBytes + lane * 128;
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 64) {
+            stores_read();                         // what lay here before has been read
+            __syncwarp();
+#pragma unroll
+            for (int z = 0; z < 8; z += 4) {
+              float o[32];
+              tmem_ld32(o_col0 + c + 8 * z, o);
+              tmem_wait_ld(o, 32);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] *= inv;
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(row_at + (((z + x) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                               pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane < queries) store_box(&tm_out, c, head, row0 + lane, sm + kTurnAt + warp * kTurnBytes + lane * 1024);
+          }
+        } else {
+          const Place at_o = whole ? own_place(work, plan.B, row0 + (lane >> 3), head >> 3, !(sg.flags & kSegGroup))
+                                   : slot_place(work, wide, sg.slot, wide ? warp : wq, lane >> 3);
+          float* const to = work.o + at_o.o + (lane & 7) * 4;
+          const bool valid = (lane >> 3) < queries;
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 32) {
+            float o[32];
+            tmem_ld32(o_col0 + c, o);
+            tmem_wait_ld(o, 32);
+            if (valid) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                *reinterpret_cast<float4*>(to + (c / 4 + x) * at_o.stride) =
+                    make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+            }
+          }
+          if (valid) work.lse[at_o.lse + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
+        }
+        tcgen05_fence_before();
+        if (kPrefix && lane < queries) {   // where the merge finds the partials
+          const int part = (sg.flags & kSegGroup) ? 0 : 2, pairs = plan.B * kNumKVHeads;
+          int* const ends = work.ends + (row0 + lane) * kNumKVHeads + (head >> 3);
+          if (j0 == 0)
+            ends[part * pairs] = final ? kNone
+                                       : (sg.slot >> 1) | (wide ? kEndWide : 0) |
+                                             (((wide ? warp : wq) * 4 + lane) << kEndPlace) | (whole ? kEndWhole : 0);
+          if (j0 + n == sg.all) ends[(part + 1) * pairs] = sg.slot >> 1;
+          if (sg.flags & kSegAlone) ends[0] = kNone;
+        }
+      }
+      if (kFold && !(sg.flags & kSegWhole)) {
+        // Few queries a sequence: the share that adds a tile's last units folds
+        // its rows, a quarter of the dims a warp.
+        int* const verdict = reinterpret_cast<int*>(smem + kVerdictAt) + w;
+        __threadfence();
+        ok = meet();                               // the partial is written
+        if (!ok) break;
+        if (wq == 0 && lane == 0) {
+          int* const count = work.count + sg.lo;
+          __threadfence();
+          const bool last = atomicAdd(count, n) + n == sg.all;
+          if (last) *count = 0;
+          *verdict = last;
+        }
+        ok = meet();
+        if (!ok) break;
+        if (*verdict) {
+          __threadfence();
+          const int lo = sg.lo, cnt = sg.cnt;
+          for (int i = 0; i < cnt; ++i)
+            fold_query<4, 12>(work, sg.hi - lo + 1, lane,
+                              [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), i >> 2, i & 3); },
+                              out + ((static_cast<int64_t>(sg.row) + i) * kNumQHeads + sg.head) * kHeadDim, wq);
+        }
+      }
+      tcgen05_fence_before();
+      seg_done(share, k);
     }
     stores_done();
   }
@@ -1413,8 +1413,10 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   __syncthreads();
   if (tid < 6 && *reinterpret_cast<const volatile int*>(smem + kAbortAt)) {
     // A wait ran out: what the merge would read may be a former call's.
+    const int grid_wide = *reinterpret_cast<const volatile int*>(smem + kGridWAt);
+    const int me = blockIdx.x, turned = me - grid_wide + (me < grid_wide ? gridDim.x : 0);
     if (kPrefix) *work.ok = 0;
-    else if (!kFold) work.parts[tid < 2 ? 2 * me + tid : 2 * kMaxCtas + 4 * me + tid - 2] = make_int4(0, 0, 0, 0);
+    else if (!kFold) work.parts[tid < 2 ? 2 * me + tid : 2 * kMaxCtas + 4 * turned + tid - 2] = make_int4(0, 0, 0, 0);
   }
   if (warp == kMmaWarp) {
     tcgen05_fence_after();
@@ -1578,7 +1580,7 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   // As many CTAs as the most that there can be to do is worth, one per SM.
   const int most = sms < kMaxCtas ? sms : kMaxCtas;
   const int64_t want = (most_units + kMinShare - 1) / kMinShare;
-  const int grid = want < most ? static_cast<int>(want) : most;
+  const int grid = want < most ? (want < 2 ? 2 : static_cast<int>(want)) : most;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(out);
   launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, tm_out, plan, work,
