@@ -608,8 +608,9 @@ struct Place {
   int stride;
 };
 __device__ __forceinline__ Place slot_place(const Work& w, int wide, int slot, int block, int query) {
-  const int rows = w.block_rows[wide];
-  const int64_t first = w.slots[wide] + static_cast<int64_t>(slot) * w.rows[wide] + block * rows;
+  // (Not by index: the structure would move to local memory.)
+  const int rows = wide ? w.block_rows[1] : w.block_rows[0];
+  const int64_t first = (wide ? w.slots[1] : w.slots[0]) + static_cast<int64_t>(slot) * (wide ? w.rows[1] : w.rows[0]) + block * rows;
   return {first * kHeadDim + query * (kGroup * 4), first + query * kGroup, rows * 4};
 }
 // Prefix mode, a whole tile's: of a sequence's prefix, or of its own tokens.
@@ -1426,37 +1427,43 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
 // ---- the merge kernels --------------------------------------------------------
 // Window mode.  The queries of a split tile are shared out over the slots that
-// hold its partials.  CTA (x, y) for x below 2 grid: slot x of the wide shares, 2
-// warps (half the dims each) to a query, 16 queries of a tile in two parts at
-// once over y (a CTA of 8 warps per share took 20 us more at 4096 tokens);
-// further x: 2 slots of the narrow shares, 4 warps (a quarter of the dims each) to
-// a query, since such a tile can have a partial for every few units.
-constexpr int kMergeWarps = 8, kMergeY = 4;
-__global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) {
+// hold its partials.  The first kMergeY x 2 grid CTAs: kMergeY to a slot of the wide
+// shares, 2 warps (half the dims each) to a query; the others: 2 slots of the
+// narrow shares, 4 warps (a quarter of the dims each) to a query, since such a tile
+// can have a partial for every few units.  Most CTAs find nothing to do, so it
+// counts how many there are and how many an SM holds: over 1000 queries the call
+// takes 37 us with 2 to a slot and 2 on an SM, 42 with 4 and 1 (149 registers, 12
+// partials at a time instead of 8).
+constexpr int kMergeWarps = 8, kMergeY = 2;
+__global__ void __launch_bounds__(32 * kMergeWarps, 2) window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wide = static_cast<int>(blockIdx.x) < 2 * grid;
-  const int slot = wide ? blockIdx.x : (blockIdx.x - 2 * grid) * 2 + (warp >> 2);
-  if (!wide && blockIdx.y) return;
+  const int rest = static_cast<int>(blockIdx.x) - kMergeY * 2 * grid;
+  const int wide = rest < 0;
+  const int slot = wide ? blockIdx.x / kMergeY : rest * 2 + (warp >> 2);
   const uint4 a = ld_dep(reinterpret_cast<const uint4*>(work.parts + (wide ? 0 : 2 * kMaxCtas) + slot));
   if (!a.w) return;
   const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
   const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
-  const int first = wide ? blockIdx.y * (kMergeWarps / 2) + (warp >> 1) : 0, step = wide ? kMergeY * kMergeWarps / 2 : 1;
+  const int first = wide ? blockIdx.x % kMergeY * (kMergeWarps / 2) + (warp >> 1) : 0, step = wide ? kMergeY * kMergeWarps / 2 : 1;
   for (int q = (slot >> 1) - lo + n * first; q < cnt; q += n * step) {
     const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
     const auto at = [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); };
     __nv_bfloat16* const to = out + ((static_cast<int64_t>(a.x) + q) * kNumQHeads + static_cast<int>(a.y) * kGroup) * kHeadDim;
     if (wide) fold_query<2, 4>(work, n, lane, at, to, warp & 1);
-    else fold_query<4, 12>(work, n, lane, at, to, warp & 3);
+    else fold_query<4, 8>(work, n, lane, at, to, warp & 3);
   }
 }
 
 // Prefix mode: a CTA of 4 warps per (sequence, KV head), a quarter of the dims
 // each: the partials of its group's tile, then those of its own tokens.
+// kBatch partials at a time: 16 while the CTAs of 2 an SM are all that there are,
+// 8 beyond.  16 (8): 9 sequences 19.6 (21.8) us, 32 over a prefix of 32768 tokens 54
+// (55), 128 under 16 prefixes of up to 1000 45.8 (42.7).
 constexpr int kFoldParts = 4;
-__global__ void __launch_bounds__(32 * kFoldParts) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
+template <int kBatch>
+__global__ void __launch_bounds__(32 * kFoldParts, kBatch > 8 ? 2 : 4) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -1470,7 +1477,7 @@ __global__ void __launch_bounds__(32 * kFoldParts) prefix_merge_kernel(const Wor
     return first == kNone ? 0 : first & kEndWhole ? 1 : last - (first & kEndShare) + 1;
   };
   const int n0 = many(ends[0], ends[1]), n1 = many(ends[2], ends[3]);
-  fold_query<kFoldParts, 16>(work, n0 + n1, lane,
+  fold_query<kFoldParts, kBatch>(work, n0 + n1, lane,
              [&](int i) {
                const bool own = i >= n0;
                const int first = own ? ends[2] : ends[0];
@@ -1586,10 +1593,10 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, tm_out, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
-    launch_pdl(true, prefix_merge_kernel, dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work,
-               plan.B, o);
+    launch_pdl(true, plan.B * kNumKVHeads > 2 * sms ? prefix_merge_kernel<8> : prefix_merge_kernel<16>,
+               dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work, plan.B, o);
   else if (kMode == kWindow)
-    launch_pdl(true, window_merge_kernel, dim3(4 * grid, kMergeY),
+    launch_pdl(true, window_merge_kernel, dim3((2 * kMergeY + 2) * grid),
                dim3(32 * kMergeWarps), 0, s, work, grid, o);
   return launch_status();
 }
