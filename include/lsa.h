@@ -667,8 +667,7 @@ int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const 
  * the other queries of the same 32 (a prompt's) that do not.
  * The work is cut into equal shares whatever the batch, and the partials of a
  * query are joined in a fixed order: repeated calls are bit-identical.  One
- * kernel (max_q <= 8 and at most 2 B) or two, programmatic dependents of their
- * predecessor.
+ * kernel (max_q 1) or two, programmatic dependents of their predecessor.
  * Device errors: CAPACITY (cu_q not starting at 0, decreasing, past T, or an nq above max_q:
  * nothing is computed), BAD_COUNT (seq_len outside [0, 64 max_chunks]: that
  * sequence's rows are zeros), BAD_SLOT (that chunk is read as zeros), TIMEOUT.

@@ -73,7 +73,7 @@ constexpr int kAhead = 4;                    // places for segments that a plann
 constexpr int kMaxCtas = LSA_POOL_ATTN_MAX_CTAS;
 constexpr int kTileCost = 3;                 // 2 to 5 measured alike
 constexpr int kMinShare = 3;                 // smallest share of a list worth a pipeline (or a CTA) of its own: one token
-                                             // over 4096 takes 16.6 us with 2, 16.0 with 3, 16.2 with 4, 16.8 with 6
+                                             // over 4096 takes 14.9 us with 2, 14.2 with 3, 14.5 with 4
 // What a wide unit costs on a CTA, in narrow ones (two pipelines, each with its own).
 // Shared prefixes, groups x sequences over prefix + own tokens: 24 over 8000 + 100
 // take 26.2 us (1.5: 27.0, 2.3: 26.2), 64 over 8000 + 2000 64 (70, 67), 5 x 26 over
@@ -95,11 +95,10 @@ struct Plan {
   int max_q, window, sinks;
   int64_t n_slots;
 };
-// What a launch can meet: a window call whose sequences have at most kNarrowQ
-// queries (narrow tiles only) and few partials to a tile, which are folded in the
-// kernel; any window call; a prefix call.  Each has only its own code: the softmax
-// loop has no registers to spare.
-enum Mode { kWindowNarrow, kWindow, kPrefixes };
+// What a launch can meet: a window call whose sequences have one query each
+// (narrow tiles only, folded in the kernel), any window call, a prefix call.  Each
+// has only its own code: the softmax loop has no registers to spare.
+enum Mode { kWindowToken, kWindow, kPrefixes };
 
 // Partials.  A share can hold the end, or a middle, of a tile that began in an
 // earlier one, and the start of a tile that goes on in the next: share c has a
@@ -113,7 +112,7 @@ struct Work {
   int64_t slots[2];  // first row of the narrow slots, of the wide ones
   int rows[2];       // rows of a narrow slot, of a wide one
   int block_rows[2]; // rows of one of its blocks
-  int* count;        // kWindowNarrow: [2 kMaxCtas], by a tile's first share: units that its partials
+  int* count;        // kWindowToken: [2 kMaxCtas], by a tile's first share: units that its partials
                      // hold so far, zero between calls
   int4* parts;       // kWindow: by slot (wide, then narrow), its tile: first query, KV head,
                      // first and last share, queries (0: no partial)
@@ -739,7 +738,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_q16, const __grid_constant__ CUtensorMap tm_q8,
                  const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_out, const Plan plan, const Work work, float scale_log2,
                  __nv_bfloat16* __restrict__ out, unsigned* status) {
-  constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowNarrow, kHasWide = kMode != kWindowNarrow;
+  constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowToken, kHasWide = kMode != kWindowToken;
   extern __shared__ __align__(1024) uint8_t smem[];
   // (The warp's index by a shuffle: the compiler has to know that it is the same in
   // every lane, or the products' operands are moved to uniform registers one by one.)
@@ -1380,8 +1379,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
       }
       if (kFold && !(sg.flags & kSegWhole)) {
-        // Few queries a sequence: the share that adds a tile's last units folds
-        // its rows, a quarter of the dims a warp.
+        // One query a tile: the share that adds its last units folds the partials, a
+        // quarter of the dims a warp.
         int* const verdict = reinterpret_cast<int*>(smem + kVerdictAt) + w;
         __threadfence();
         ok = meet();                               // the partial is written
@@ -1397,11 +1396,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (!ok) break;
         if (*verdict) {
           __threadfence();
-          const int lo = sg.lo, cnt = sg.cnt;
-          for (int i = 0; i < cnt; ++i)
-            fold_query<4, 12>(work, sg.hi - lo + 1, lane,
-                              [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), i >> 2, i & 3); },
-                              out + ((static_cast<int64_t>(sg.row) + i) * kNumQHeads + sg.head) * kHeadDim, wq);
+          const int lo = sg.lo;
+          fold_query<4, 12>(work, sg.hi - lo + 1, lane, [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), 0, 0); },
+                            out + (static_cast<int64_t>(sg.row) * kNumQHeads + sg.head) * kHeadDim, wq);
         }
       }
       tcgen05_fence_before();
@@ -1640,12 +1637,11 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
   const int64_t seen = static_cast<int64_t>(plan.window) / kChunkTokens + 3 + plan.sinks / kChunkTokens + 1;
   const int64_t tiles = T / pool::kWideQ + B;
   const int64_t units = kNumKVHeads * tiles * ((seen < max_chunks ? seen : max_chunks) + pool::kTileCost);
-  // Partials that one SM folds: max_q for each of a tile's shares, at most 2 x 148 /
-  // 8 B of them.  One kernel (two) takes 14 (19) us for 1 query over 4096 tokens,
-  // 20.4 (19.6) for 4, 29 (20) for 8; 30 (23) for 8 of 2 sequences each; 20 (21) for
-  // 8 of 4 each with a window of 1024, 63 (70) of 64.
-  return max_q <= pool::kNarrowQ && max_q <= 2 * B
-             ? pool::launch<pool::kWindowNarrow>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream)
+  // Folded in the kernel (by a second one): 14.1 (15.7) us for one token over 4096,
+  // 22.5 (23.8) over 20000; but 26.2 (24.2) for 2 queries over 20000, 21.6 (20.4) for
+  // 4 of 4 sequences each, 36 (32) for 8 of 8.
+  return max_q == 1
+             ? pool::launch<pool::kWindowToken>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream)
              : pool::launch<pool::kWindow>(plan, work, q, k_pool, v_pool, softmax_scale, out, units, stream);
 }
 
