@@ -46,12 +46,12 @@
 // product are theirs.
 //
 // What bounds it.  Narrow shares: memory (one token over 100000: 70.6 us, 5.8 TB/s,
-// 89% of the copy rate; 64 tokens over windows of 1024: 56 us, 4.8 TB/s, the rest is
+// 89% of the copy rate; 64 tokens over windows of 1024: 54.5 us, 4.9 TB/s, the rest is
 // the start, 5 us, and the spread of the CTAs' ends).  Wide shares: the chain of a
 // unit, 1450 cycles for 128 x 2 rows, of which the tensor core is busy 1350 (with
 // 64 keys a product of scores is fed by shared memory); without the softmax's
 // arithmetic a prompt of 4096 queries over a window of 1024 would take 92% of its
-// 141 us (0.86 PFLOP/s).  Single tokens over short contexts: latency, about 5 us until
+// 139 us (0.87 PFLOP/s).  Single tokens over short contexts: latency, about 5 us until
 // the first scores, 1.5 us a unit, 2 us for the fold.
 //
 // TMEM (512 columns): scores 2 pipelines x 2 buffers x 64, accumulators 2 x 128.
@@ -73,6 +73,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10;  // of pipeline 0; 9 and 11 are pipe
 constexpr int kThreads = 12 * 32;
 constexpr int kHalves = 8;                   // half-stages: a unit's K or V of one head
 constexpr int kBoxBytes = 8192;              // 64 tokens x 64 dims
+constexpr int kPartRows = 16, kPartBytes = kPartRows * 128;   // of a chunk that is not seen whole: 16 tokens x 64 dims
 constexpr int kHalfBytes = 2 * kBoxBytes;
 constexpr int kQBoxBytes = 16384;            // 128 rows x 64 dims
 constexpr int kQTileBytes = 2 * kQBoxBytes;
@@ -333,6 +334,11 @@ struct Cursor {
 // 64 bits: the lowest x.
 __device__ __forceinline__ uint64_t lowest(int x) {
   return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1;
+}
+// Window mode: tokens of the chunk that begins at token kb which some query of a
+// tile sees.
+__device__ __forceinline__ uint64_t tile_sees(const Plan& p, int kb, int p0, int cnt) {
+  return lowest(p0 + cnt - kb) & (~lowest(p0 - p.window + 1 - kb) | lowest(p.sinks - kb));
 }
 
 // Barriers and copies by shared address: a generic pointer takes two registers
@@ -744,10 +750,12 @@ __device__ __forceinline__ Ring ring_of(bool wide, int w) { return wide ? Ring{0
 template <Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ CUtensorMap tm_k_part, const __grid_constant__ CUtensorMap tm_v_part,
                  const __grid_constant__ CUtensorMap tm_q16, const __grid_constant__ CUtensorMap tm_q8,
                  const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_out, const Plan plan, const Work work, float scale_log2,
                  __nv_bfloat16* __restrict__ out, unsigned* status) {
-  constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowToken, kHasWide = kMode != kWindowToken;
+  constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowToken, kHasWide = !kFold;
+  constexpr bool kParts = !kPrefix;   // chunks that are not seen whole are loaded by parts
   extern __shared__ __align__(1024) uint8_t smem[];
   // (The warp's index by a shuffle: the compiler has to know that it is the same in
   // every lane, or the products' operands are moved to uniform registers one by one.)
@@ -785,8 +793,14 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   if (tid == kLoadWarp * 32) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_q16);
-    tma_prefetch_desc(&tm_q8);
+    if (kParts) {
+      tma_prefetch_desc(&tm_k_part);
+      tma_prefetch_desc(&tm_v_part);
+    }
+    if (kHasWide) {
+      tma_prefetch_desc(&tm_q16);
+      tma_prefetch_desc(&tm_q8);
+    }
     tma_prefetch_desc(&tm_q1);
     tma_prefetch_desc(&tm_out);
   }
@@ -988,13 +1002,19 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       }
       const Ring ring = ring_of(wide, w);
       unsigned halves = 0;   // loads so far
-      // K and V of a segment's units, the next ones of the share.
-      auto load_units = [&](int units, int flags, int j0, int first, int low, int g, const int32_t* table, int64_t ident) {
+      // K and V of a segment's units, the next ones of the share.  In window mode only
+      // the parts (16 tokens) of a chunk with a token in sight are loaded; what the
+      // other rows hold is masked (K) and zeroed (V).  64 single tokens over windows of
+      // 1024 take 54.4 us so, 56.5 with whole chunks (300 MB for 269), a prompt of 4096
+      // 139.7 and 142.9.  A prefix call has only ends of sequences to save on, and
+      // takes longer by more but smaller loads (128 sequences, 5 groups: 80.1, 77.5).
+      auto load_units = [&](int units, int flags, int j0, int first, int low, int g, const int32_t* table, int64_t ident, int p0,
+                            int cnt) {
         // Another tile of the entry reads the same chunks: they stay in L2.
         const uint64_t policy = (flags & kSegAgain) ? policy_again : policy_once;
         int row = 0;
         for (int i = 0; i < units; ++i) {
-          if ((i & 31) == 0) {   // the rows of 32 units at a time, a lane each
+          if ((i & 31) == 0) {   // 32 units at a time, a lane each: the pool row (a multiple of 64) and 4 bits, the parts
             row = beyond;
             if (!(flags & kSegEmpty) && i + lane < units) {
               const int j = j0 + i + lane, c = j < first ? j : low + j - first;
@@ -1003,9 +1023,13 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 row = (static_cast<int>(slot) * kNumKVHeads + g) * kChunkTokens;
               else
                 set_status(status, LSA_DEV_ERR_BAD_SLOT);
+              const uint64_t seen = tile_sees(plan, c * kChunkTokens, p0, cnt);
+              const uint32_t lo = static_cast<uint32_t>(seen), hi = static_cast<uint32_t>(seen >> 32);
+              if (kParts) row |= ((lo & 0xffff) != 0) | (lo >> 16 != 0) << 1 | ((hi & 0xffff) != 0) << 2 | (hi >> 16 != 0) << 3;
             }
           }
-          const int y = __shfl_sync(0xffffffffu, row, i & 31);
+          const int of_unit = __shfl_sync(0xffffffffu, row, i & 31);
+          const int y = of_unit & ~63, parts = kParts ? of_unit & 15 : 15;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const unsigned h = ring.half(halves);
@@ -1013,10 +1037,20 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (halves > ring.mask && !wait(kEmpty + 8 * h, ring.parity(halves) ^ 1)) return false;
             if (lane == 0) {
               const uint32_t dst = sm + h * kHalfBytes, bar = sm + kFull + 8 * h;
-              const CUtensorMap* const map = kv ? &tm_v : &tm_k;
-              bar_expect(bar, kHalfBytes);
-              load_box(dst, map, 0, y, bar, policy);
-              load_box(dst + kBoxBytes, map, 64, y, bar, policy);
+              if (parts == 15) {
+                const CUtensorMap* const map = kv ? &tm_v : &tm_k;
+                bar_expect(bar, kHalfBytes);
+                load_box(dst, map, 0, y, bar, policy);
+                load_box(dst + kBoxBytes, map, 64, y, bar, policy);
+              } else {
+                const CUtensorMap* const map = kv ? &tm_v_part : &tm_k_part;
+                bar_expect(bar, __popc(parts) * 2 * kPartBytes);
+                for (int b = 0; b < 4; ++b) {
+                  if (!((parts >> b) & 1)) continue;
+                  load_box(dst + b * kPartBytes, map, 0, y + b * kPartRows, bar, policy);
+                  load_box(dst + kBoxBytes + b * kPartBytes, map, 64, y + b * kPartRows, bar, policy);
+                }
+              }
             }
             __syncwarp();
             // A wide share's first K comes alone: every CTA starts at once, and with
@@ -1042,12 +1076,12 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           ok = seg_get(0, k);
           if (!ok) break;
           const Seg& s = segs[k % kAhead];
-          const int units = s.units, flags = s.flags, j0 = s.j0, first = s.first, low = s.low, g = s.g;
+          const int units = s.units, flags = s.flags, j0 = s.j0, first = s.first, low = s.low, g = s.g, p0 = s.p0, cnt = s.cnt;
           const int32_t* const table = s.table;
           const int64_t ident = s.ident;
           seg_done(0, k);
           if (units == 0) break;
-          ok = load_units(units, flags, j0, first, low, g, table, ident);
+          ok = load_units(units, flags, j0, first, low, g, table, ident, p0, cnt);
         }
         if (!ok && lane == 0) land();
       } else if (wide) {
@@ -1086,7 +1120,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         begin(1 + w, part_n, total[0], 2 * turned + w);
         for (unsigned k = 0; ok; ++k) {
           const int units = more ? cur.units() : 0, cnt = cur.cnt, row = cur.row(false), j0 = cur.j, first = cur.first,
-                    low = cur.low, g = cur.g, flags = cur.empty ? kSegEmpty : 0;
+                    low = cur.low, g = cur.g, flags = cur.empty ? kSegEmpty : 0, p0 = cur.p0;
           const int32_t* const table = cur.s.table;
           const int64_t ident = cur.s.ident;
           ok = publish(1 + w, part_n, 2 * turned + w);
@@ -1096,14 +1130,15 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           if (!ok) break;
           if (lane == 0) {
             const uint32_t bar = sm + kNFull + 16 * w + 8 * b, q = sm + kQAt + w * kQTileBytes + b * kQ2Bytes;
-            const CUtensorMap* const map = cnt == 1 ? &tm_q1 : &tm_q8;   // what other rows hold is not read back
-            bar_expect(bar, 2 * 128 * kGroup * (cnt == 1 ? 1 : kNarrowQ));
+            const bool one = kFold || cnt == 1;       // (what other rows hold is not read back)
+            const CUtensorMap* const map = one ? &tm_q1 : &tm_q8;
+            bar_expect(bar, 2 * 128 * kGroup * (one ? 1 : kNarrowQ));
             load_box(q, map, 0, g * kGroup, row, bar);
             load_box(q + kQBoxBytes, map, 64, g * kGroup, row, bar);
           }
           __syncwarp();
           ++loads;
-          ok = load_units(units, flags, j0, first, low, g, table, ident);
+          ok = load_units(units, flags, j0, first, low, g, table, ident, p0, cnt);
           advance(1 + w, part_n, 2 * turned + w);
         }
         if (!ok && lane == 0) {   // copies in flight land before the CTA ends
@@ -1222,7 +1257,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             any = see = lowest(sg.len - kb);
           } else {
             const int pos = sg.p0 + i_first + (lane >> 3) - kb;   // of the row's query, in the unit
-            any = lowest(sg.p0 + sg.cnt - kb) & (~lowest(sg.p0 - plan.window + 1 - kb) | lowest(plan.sinks - kb));
+            any = tile_sees(plan, kb, sg.p0, sg.cnt);
             see = lowest(pos + 1) & (~lowest(pos - plan.window + 1) | lowest(plan.sinks - kb));
           }
           if (any != ~0ull) {
@@ -1531,10 +1566,10 @@ size_t prefix_layout(Work* w, void* at, int B) {
 std::mutex g_mu;
 bool g_attr_set[3][64] = {};
 
-int encode_pool(CUtensorMap* map, const void* base, int64_t n_slots) {
+int encode_pool(CUtensorMap* map, const void* base, int64_t n_slots, int rows) {
   const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(n_slots) * kNumKVHeads * kChunkTokens};
   const cuuint64_t strides[1] = {kHeadDim * 2};
-  const cuuint32_t box[2] = {64, kChunkTokens}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)}, estr[2] = {1, 1};
   return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -1569,7 +1604,7 @@ template <Mode kMode>
 int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool, const void* v_pool, float scale, void* out,
            int64_t most_units, void* stream) {
   const int sms = device_sm_count();
-  if (sms <= 0 || !tensor_map_encoder()) return LSA_ERR_NO_DEVICE;
+  if (sms < 2 || !tensor_map_encoder()) return LSA_ERR_NO_DEVICE;   // (wide and narrow tiles have CTAs of their own)
   int dev = 0;
   cudaGetDevice(&dev);
   {
@@ -1582,11 +1617,17 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
       g_attr_set[kMode][dev] = true;
     }
   }
-  CUtensorMap tm_k, tm_v, tm_q16, tm_q8, tm_q1, tm_out;
-  int st = encode_pool(&tm_k, k_pool, plan.n_slots);
-  if (st == LSA_OK) st = encode_pool(&tm_v, v_pool, plan.n_slots);
-  if (st == LSA_OK) st = encode_q(&tm_q16, q, plan.rows, kWideQ / 2);
-  if (st == LSA_OK) st = encode_q(&tm_q8, q, plan.rows, kNarrowQ);
+  CUtensorMap tm_k, tm_v, tm_k_part = {}, tm_v_part = {}, tm_q16 = {}, tm_q8 = {}, tm_q1, tm_out;
+  int st = encode_pool(&tm_k, k_pool, plan.n_slots, kChunkTokens);
+  if (st == LSA_OK) st = encode_pool(&tm_v, v_pool, plan.n_slots, kChunkTokens);
+  if (kMode != kPrefixes) {
+    if (st == LSA_OK) st = encode_pool(&tm_k_part, k_pool, plan.n_slots, kPartRows);
+    if (st == LSA_OK) st = encode_pool(&tm_v_part, v_pool, plan.n_slots, kPartRows);
+  }
+  if (kMode != kWindowToken) {   // single tokens have neither wide tiles nor others than of one query
+    if (st == LSA_OK) st = encode_q(&tm_q16, q, plan.rows, kWideQ / 2);
+    if (st == LSA_OK) st = encode_q(&tm_q8, q, plan.rows, kNarrowQ);
+  }
   if (st == LSA_OK) st = encode_q(&tm_q1, q, plan.rows, 1);
   if (st == LSA_OK) st = encode_q(&tm_out, out, plan.rows, 1);
   if (st != LSA_OK) return st;
@@ -1596,7 +1637,8 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   const int grid = want < most ? (want < 2 ? 2 : static_cast<int>(want)) : most;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(out);
-  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_q16, tm_q8, tm_q1, tm_out, plan, work,
+  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_k_part, tm_v_part, tm_q16, tm_q8, tm_q1,
+             tm_out, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
     launch_pdl(true, plan.B * kNumKVHeads > 2 * sms ? prefix_merge_kernel<8> : prefix_merge_kernel<16>,
