@@ -624,7 +624,8 @@ struct Place {
 __device__ __forceinline__ Place slot_place(const Work& w, int wide, int slot, int block, int query) {
   // (Not by index: the structure would move to local memory.)
   const int rows = wide ? w.block_rows[1] : w.block_rows[0];
-  const int64_t first = (wide ? w.slots[1] : w.slots[0]) + static_cast<int64_t>(slot) * (wide ? w.rows[1] : w.rows[0]) + block * rows;
+  const int64_t slot_rows = wide ? w.rows[1] : w.rows[0];
+  const int64_t first = (wide ? w.slots[1] : w.slots[0]) + slot * slot_rows + block * rows;
   return {first * kHeadDim + query * (kGroup * 4), first + query * kGroup, rows * 4};
 }
 // Prefix mode, a whole tile's: of a sequence's prefix, or of its own tokens.
@@ -752,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_k_part, const __grid_constant__ CUtensorMap tm_v_part,
                  const __grid_constant__ CUtensorMap tm_q16, const __grid_constant__ CUtensorMap tm_q8,
-                 const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_out, const Plan plan, const Work work, float scale_log2,
-                 __nv_bfloat16* __restrict__ out, unsigned* status) {
+                 const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_out, const Plan plan,
+                 const Work work, float scale_log2, __nv_bfloat16* __restrict__ out, unsigned* status) {
   constexpr bool kPrefix = kMode == kPrefixes, kFold = kMode == kWindowToken, kHasWide = !kFold;
   constexpr bool kParts = !kPrefix;   // chunks that are not seen whole are loaded by parts
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1008,8 +1009,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       // 1024 take 54.4 us so, 56.5 with whole chunks (300 MB for 269), a prompt of 4096
       // 139.7 and 142.9.  A prefix call has only ends of sequences to save on, and
       // takes longer by more but smaller loads (128 sequences, 5 groups: 80.1, 77.5).
-      auto load_units = [&](int units, int flags, int j0, int first, int low, int g, const int32_t* table, int64_t ident, int p0,
-                            int cnt) {
+      auto load_units = [&](int units, int flags, int j0, int first, int low, int g, const int32_t* table, int64_t ident,
+                            int p0, int cnt) {
         // Another tile of the entry reads the same chunks: they stay in L2.
         const uint64_t policy = (flags & kSegAgain) ? policy_again : policy_once;
         int row = 0;
@@ -1302,7 +1303,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           mx[0] = max3(mx[0], s[60], s[61]);
           mx[1] = max3(mx[1], s[62], s[63]);
           const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
-          const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;   // a row's first score that is not masked always does
+          // (A row's first score that is not masked always does.)
+          const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;
           if (__any_sync(0xffffffffu, raise)) {
             const float m_new = raise ? top : m;
             const float f = raise ? fast_exp2(m - m_new) : 1.f;
@@ -1441,7 +1443,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (*verdict) {
           __threadfence();
           const int lo = sg.lo;
-          fold_query<4, 12>(work, sg.hi - lo + 1, lane, [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), 0, 0); },
+          fold_query<4, 12>(work, sg.hi - lo + 1, lane,
+                            [&](int x) { return slot_place(work, 0, 2 * (lo + x) + (x == 0), 0, 0); },
                             out + (static_cast<int64_t>(sg.row) * kNumQHeads + sg.head) * kHeadDim, wq);
         }
       }
@@ -1476,7 +1479,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // takes 37 us with 2 to a slot and 2 on an SM, 42 with 4 and 1 (149 registers, 12
 // partials at a time instead of 8).
 constexpr int kMergeWarps = 8, kMergeY = 2;
-__global__ void __launch_bounds__(32 * kMergeWarps, 2) window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(32 * kMergeWarps, 2)
+window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1487,7 +1491,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) window_merge_kernel(const
   if (!a.w) return;
   const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
   const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
-  const int first = wide ? blockIdx.x % kMergeY * (kMergeWarps / 2) + (warp >> 1) : 0, step = wide ? kMergeY * kMergeWarps / 2 : 1;
+  const int first = wide ? blockIdx.x % kMergeY * (kMergeWarps / 2) + (warp >> 1) : 0;
+  const int step = wide ? kMergeY * kMergeWarps / 2 : 1;
   for (int q = (slot >> 1) - lo + n * first; q < cnt; q += n * step) {
     const int i = q < half ? q : q - half, block = (q < half ? 0 : 4) + (i >> 2);
     const auto at = [&](int k) { return slot_place(work, wide, 2 * (lo + k) + (k == 0), block, i & 3); };
@@ -1504,7 +1509,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) window_merge_kernel(const
 // (55), 128 under 16 prefixes of up to 1000 45.8 (42.7).
 constexpr int kFoldParts = 4;
 template <int kBatch>
-__global__ void __launch_bounds__(32 * kFoldParts, kBatch > 8 ? 2 : 4) prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(32 * kFoldParts, kBatch > 8 ? 2 : 4)
+prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -1637,8 +1643,8 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   const int grid = want < most ? (want < 2 ? 2 : static_cast<int>(want)) : most;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(out);
-  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_k_part, tm_v_part, tm_q16, tm_q8, tm_q1,
-             tm_out, plan, work,
+  launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_k_part, tm_v_part,
+             tm_q16, tm_q8, tm_q1, tm_out, plan, work,
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
     launch_pdl(true, plan.B * kNumKVHeads > 2 * sms ? prefix_merge_kernel<8> : prefix_merge_kernel<16>,
