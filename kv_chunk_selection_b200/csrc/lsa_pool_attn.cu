@@ -51,7 +51,7 @@
 // unit, 1450 cycles for 128 x 2 rows, of which the tensor core is busy 1350 (with
 // 64 keys a product of scores is fed by shared memory); without the softmax's
 // arithmetic a prompt of 4096 queries over a window of 1024 would take 92% of its
-// 139 us (0.87 PFLOP/s).  Single tokens over short contexts: latency, about 5 us until
+// 137 us (0.88 PFLOP/s).  Single tokens over short contexts: latency, about 5 us until
 // the first scores, 1.5 us a unit, 2 us for the fold.
 //
 // TMEM (512 columns): scores 2 pipelines x 2 buffers x 64, accumulators 2 x 128.
@@ -1269,12 +1269,13 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const unsigned vx = 2 * (job + i) + 1, h = ring.half(vx);
             ok = wait(kFull + 8 * h, ring.parity(vx));
             if (!ok) break;
-            uint8_t* const vs = smem + h * kHalfBytes;
-            for (int x = wq * 32 + lane; x < kChunkTokens * 16; x += 128) {
-              const int row = x >> 4;
-              if (!((any >> row) & 1))
-                *reinterpret_cast<uint4*>(vs + ((x >> 3) & 1) * kBoxBytes + row * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
+            // (Thread t of the warpgroup: piece t % 16 of rows t / 16 + 8 x.)
+            const int t = wq * 32 + lane;
+            uint8_t* const vs = smem + h * kHalfBytes + ((t >> 3) & 1) * kBoxBytes + (t >> 4) * 128 + (t & 7) * 16;
+            const uint64_t rows = any >> (t >> 4);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (!((rows >> (8 * x)) & 1)) *reinterpret_cast<uint4*>(vs + x * 1024) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
           }
         }
