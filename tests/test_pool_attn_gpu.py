@@ -63,6 +63,20 @@ def test_long_prompt_is_split_over_the_chip(window, sinks):
     clean()
 
 
+@pytest.mark.parametrize("nq", [1, 3, 40])
+def test_chunks_seen_in_part_after_a_call_of_nan(nq):
+    """Windows and sinks that end around the 16-token parts of a chunk, right after a call whose K and V are NaN:
+    what it left in the SMs' shared memory lies in the rows that are not loaded."""
+    for window in (1, 15, 16, 17, 33, 48, 100):
+        for sinks in (0, 1, 16, 31, 47):
+            c = WindowCase([(nq, n) for n in (300, 333, 400, 64 + nq)], window, sinks, seed=window)
+            nan = WindowCase([(nq, 300)] * 8, 1 << 20, 0)
+            nan.d_k.fill_(float("nan")), nan.d_v.fill_(float("nan"))
+            assert bool(nan.call().isnan().all())
+            c.check(c.call())
+    clean()
+
+
 def test_queries_before_the_first_token_and_empty_sequences():
     # five queries but three cached tokens: the first two see nothing
     c = WindowCase([(5, 5), (0, 100), (4, 4), (0, 0), (40, 40)], 8, 2, spare_rows=1)
