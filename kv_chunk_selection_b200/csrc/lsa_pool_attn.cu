@@ -59,6 +59,7 @@
 // so a page's unwritten tail may hold anything (0 times NaN is NaN); the scores
 // there are masked by selection.
 #include <math.h>
+#include <math_constants.h>
 
 #include <mutex>
 
@@ -1310,7 +1311,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           // (A row's first score that is not masked always does.)
           const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;
           if (__any_sync(0xffffffffu, raise)) {
-            const float m_new = raise ? top : m;
+            // A maximum of +inf is no number from here on: inf - inf is none in the
+            // formula either, and the powers on the FMA pipe would make zeros of it.
+            const float m_new = raise ? (top == INFINITY ? CUDART_NAN_F : top) : m;
             const float f = raise ? fast_exp2(m - m_new) : 1.f;
             m = m_new;
             l *= f;
