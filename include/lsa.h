@@ -644,8 +644,10 @@ int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const 
  *
  *   out[t,h,:] = sum_j softmax_j(scale * q[t,h,:] . k_j) v_j
  *
- * A query that sees nothing (nq > seq_len: positions below 0) gets zeros.  A
- * window of at least seq_len is causal attention over all cached tokens.
+ * A query that sees nothing (nq > seq_len: positions below 0) gets zeros; one
+ * that sees a score of +inf or NaN, or scores of -inf only, gets NaN, as the
+ * formula does.  A window of at least seq_len is causal attention over all
+ * cached tokens.
  *   q           device bf16 [T][64][128]; out device bf16 [T][64][128] (fp32
  *               sums and softmax; the probabilities are rounded once to bf16
  *               for the tensor cores, the output once).  Rows at or past
@@ -692,7 +694,7 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
  * The prefix is read once per KV head for every 32 sequences of its group and
  * multiplied with all of their queries together.  Sequences from
  * cu_group[n_groups] on belong to no group: they attend their own tokens only.
- * A sequence with no token at all gets zeros.
+ * A sequence with no token at all gets zeros (infinite scores as above).
  *   q            device bf16 [B][64][128]; out device bf16 [B][64][128]
  *                (rounded as by lsa_window_attn)
  *   prefix_table device int32 [n_groups][max_prefix_chunks], slots of the

@@ -95,6 +95,11 @@ constexpr int kMinShare = 3;                 // smallest share of a list worth a
 constexpr float kWideCost = 1.8f;
 constexpr int kFmaEvery = 4;                 // of the pairs of powers of two, one in 4 on the FMA pipe
 constexpr float kRaise = 8.f;                // growth of the maximum (log2) that rescales the accumulator
+// The maximum of a row that has seen keys whose scores are all -inf, and the
+// log-sum-exp of a partial of only such; -inf: it has seen none.  A row that ends
+// so is 0 / 0, one without a key zeros.  (Below every maximum of finite scores, so
+// that the first of them replaces it and weighs its partials 0.)
+constexpr float kLowest = -3.402823466e38f;
 constexpr int kSCols = 64, kOCol0 = 256;     // TMEM: S[w][b] at (2 w + b) * 64, O[w] at 256 + 128 w
 
 struct Plan {
@@ -691,7 +696,7 @@ __device__ __forceinline__ void fold_query(const Work& w, int n, int lane, At pl
       }
     }
   }
-  const float id = den == 0.f ? 0.f : 1.f / den;
+  const float id = m == -INFINITY ? 0.f : m == kLowest ? CUDART_NAN_F : 1.f / den;
 #pragma unroll
   for (int k = 0; k < kPieces; ++k)
     *reinterpret_cast<uint2*>(out + h * kHeadDim + 4 * (c0 + 4 * k)) =
@@ -1308,13 +1313,16 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           mx[0] = max3(mx[0], s[60], s[61]);
           mx[1] = max3(mx[1], s[62], s[63]);
           const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
-          // (A row's first score that is not masked always does.)
-          const bool raise = !(top <= m + kRaise) && (lane >> 3) < queries;
+          // (A row's first score that is not masked always does; until then every unit.)
+          const bool raise = !(top < m + kRaise) && (lane >> 3) < queries;
           if (__any_sync(0xffffffffu, raise)) {
             // A maximum of +inf is no number from here on: inf - inf is none in the
             // formula either, and the powers on the FMA pipe would make zeros of it.
-            const float m_new = raise ? (top == INFINITY ? CUDART_NAN_F : top) : m;
-            const float f = raise ? fast_exp2(m - m_new) : 1.f;
+            float m_new = m, f = 1.f;
+            if (raise) {
+              m_new = top == INFINITY ? CUDART_NAN_F : top == -INFINITY && !(edge && see == 0) ? kLowest : top;
+              f = top == -INFINITY ? 0.f : fast_exp2(m - m_new);
+            }
             m = m_new;
             l *= f;
             if (i > 0) {                           // the accumulator of earlier units follows
@@ -1370,8 +1378,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (!ok) break;
       tcgen05_fence_after();
       if (queries > 0) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool whole = sg.flags & kSegWhole, final = whole && (!kPrefix || (sg.flags & kSegAlone));
+        // (No sum: no key, or scores of -inf only; a partial says which in its log-sum-exp.)
+        const float inv = l == 0.f ? (final && m == kLowest ? CUDART_NAN_F : 0.f) : 1.f / l;
         const int row0 = sg.row + i_first, head = sg.head;   // the warp's first query, its first query head
         if (final) {
           // Output rows (query, head): 64 dims at a time through the warp's 4 KiB of
@@ -1417,7 +1426,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
             }
           }
-          if (valid) work.lse[at_o.lse + (lane & 7)] = l == 0.f ? -INFINITY : m + __log2f(l);
+          if (valid) work.lse[at_o.lse + (lane & 7)] = l == 0.f ? m : m + __log2f(l);
         }
         tcgen05_fence_before();
         if (kPrefix && lane < queries) {   // where the merge finds the partials

@@ -71,6 +71,34 @@ def test_one_infinite_key_wherever_it_stands_in_its_chunk(seqs, place):
         assert check(c) > 0                           # half of the rows, about
 
 
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("seqs,window,sinks", [([(1, 70)], 6, 0), ([(1, 3000)], 2900, 2), ([(5, 64), (1, 0), (1, 1)], 1, 0),
+                                               ([(33, 200), (40, 40)], 3, 1), ([(40, 2500)], 2000, 0)])
+def test_nothing_but_infinite_scores(seqs, window, sinks, value):
+    """All keys of all tokens: rows see +inf, or nothing but -inf, or (before the first token) nothing."""
+    c = WindowCase(seqs, window, sinks, seed=3)
+    no_zero_queries(c)
+    for b, (nq, n) in enumerate(seqs):
+        for t in range(n):
+            if bool(c.see[b][:, t].any()):
+                put(c, b, t, value)
+    assert check(c) == 64 * sum(min(nq, n) for nq, n in seqs)
+
+
+def test_only_minus_infinity_in_some_shares_of_a_split_row():
+    """The rows whose other shares hold numbers are those numbers' average."""
+    for nq in (1, 40):
+        c = WindowCase([(nq, 3000)], 1 << 20, 0, seed=nq)
+        c.q[..., 5] = c.q[..., 5].abs() + 1
+        c.d_q.copy_(c.q)
+        for t in list(range(0, 1400)) + list(range(1500, 2900)):
+            put(c, 0, t, -INF)
+        assert check(c) == 0
+        for t in list(range(1400, 1500)) + list(range(2900, 3000)):
+            put(c, 0, t, -INF)
+        assert check(c) == 64 * nq
+
+
 def test_an_unseen_infinite_key_changes_nothing():
     c = WindowCase([(40, 300), (1, 150)], 20, 0)
     good = c.call()
@@ -100,6 +128,17 @@ def test_prefixes_with_an_infinite_key(groups, suffix, place):
                         c.own[b][1][place, :, 5] = value
                         c.d_k[int(c.d_table[b, 0]), :, place, 5] = value
             check_prefix(c)
+
+
+def test_a_prefix_of_minus_infinity():
+    """With own tokens, theirs is the answer; without any, 0 / 0; no token at all stays zeros."""
+    for groups, suffix in (([(2, 64), (1, 0)], [0, 3, 0]), ([(12, 1500)], [0, 9] * 6)):
+        c = PrefixCase(groups, suffix, seed=1)
+        c.q[..., 5] = c.q[..., 5].abs() + 1
+        c.d_q.copy_(c.q)
+        c.prefix[0][1][..., 5] = -INF
+        c.d_k[c.d_prefix[0, : (groups[0][1] + 63) // 64].long(), ..., 5] = -INF
+        assert check_prefix(c) == 64 * sum(n == 0 for n in suffix[: groups[0][0]])
 
 
 def check_prefix(c):
