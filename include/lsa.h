@@ -722,6 +722,18 @@ int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool
                            int max_chunks, float softmax_scale, void* out, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/*
+ * lsa_debug_withhold_share -- fault injection for the two calls above: in the
+ * next one of this process, the CTA `cta` (modulo the grid) is never told its
+ * share of the work, and every wait of the call gives up after limit_us
+ * microseconds (1 .. 2,000,000; 1 s otherwise).  That CTA's waits run out: the
+ * call reports TIMEOUT and ends, the context stays usable, and no output row of
+ * which the CTA held a part is written (nor, where a second kernel joins the
+ * partials, any other row that is split).  cta = -1 disarms it.  For tests of
+ * the failure detection; not for a call that is captured.
+ */
+int lsa_debug_withhold_share(int cta, unsigned int limit_us);
+
 #ifdef __cplusplus
 }
 #endif

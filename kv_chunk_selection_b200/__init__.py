@@ -81,6 +81,7 @@ def _load():
         "lsa_window_attn": ([P, I64, P, P, I64, P, P, P, I, I, I, I, I, F, P, P, S, P], I),
         "lsa_prefix_attn_workspace_size": ([I, I], S),
         "lsa_prefix_decode_attn": ([P, P, P, I64, P, P, P, I, I, P, P, I, I, F, P, P, S, P], I),
+        "lsa_debug_withhold_share": ([I, ctypes.c_uint], I),
         "lsa_qk_norm_rope": ([P, I64, I64, P, P, F, P, P, I, F, ctypes.c_uint, P, P, P, P], I),
         "lsa_qk_norm_rope_pool": ([P, I64, I64, P, P, F, P, P, I, F, ctypes.c_uint, P, P, P, I64, P, P, P, I, I, P], I),
     }
@@ -832,11 +833,17 @@ def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len
         raise LsaError("lsa_prefix_decode_attn", st)
 
 
+def lsa_debug_withhold_share(cta: int, limit_us: int = 5000):
+    """The next lsa_window_attn or lsa_prefix_decode_attn: CTA ``cta`` never learns its share and its waits run out after
+    ``limit_us`` (TIMEOUT in the device status); -1 disarms it.  For tests."""
+    _check("lsa_debug_withhold_share", _load().lsa_debug_withhold_share(int(cta), int(limit_us)))
+
+
 from .rope import rope_frequencies  # noqa: E402
 
 __all__ = [
     "lsa_qk_norm_rope", "lsa_qk_norm_rope_pool", "rope_frequencies", "lsa_window_attn", "new_window_attn_workspace",
-    "lsa_prefix_decode_attn", "new_prefix_attn_workspace",
+    "lsa_prefix_decode_attn", "new_prefix_attn_workspace", "lsa_debug_withhold_share",
     "LsaError", "lib", "read_device_status", "decode_status", "lsa_index_score", "lsa_topk_chunks",
     "lsa_threshold_chunks",
     "lsa_gather_chunks", "lsa_fetch_from_host", "lsa_fetch_from_host_delta", "lsa_fetch_from_host_copy",

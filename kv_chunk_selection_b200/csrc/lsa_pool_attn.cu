@@ -61,6 +61,7 @@
 #include <math.h>
 #include <math_constants.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "lsa_common.cuh"
@@ -113,6 +114,8 @@ struct Plan {
   int max_chunks, group_chunks;
   int max_q, window, sinks;
   int64_t n_slots;
+  unsigned long long wait_ns;   // limit of every wait
+  int withheld;              // CTA whose planners write no segment (lsa_debug_withhold_share), or -1
 };
 // What a launch can meet: a window call whose sequences have one query each
 // (narrow tiles only, folded in the kernel), any window call, a prefix call.  Each
@@ -137,7 +140,7 @@ struct Work {
                      // first and last share, queries (0: no partial)
   int* ends;         // prefix mode: [4][8 B], by (sequence, KV head): first and last partial of the
                      // prefix, of the own tokens
-  int* ok;           // prefix mode: the offsets were valid
+  int* ok;           // [kMaxCtas], not kWindowToken: the CTA's partials are whole (valid offsets, no wait ran out)
 };
 // The first partial of a (sequence, KV head): its share, whether of the wide
 // list, the query's block and number there, or that the rows are in their own
@@ -381,17 +384,18 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned parity) {
       : "memory");
   return ok != 0;
 }
-// Waits, at most kWaitLimitNs, or until another role has given up; the same
+// Waits, at most limit_ns, or until another role has given up; the same
 // answer in every lane, so that the warp's collective instructions stay whole.
 // `abort_flag`: 0, or 1 once a wait of the CTA ran out.
-__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, unsigned parity, uint32_t abort_flag, unsigned* status) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, unsigned parity, uint32_t abort_flag,
+                                              unsigned long long limit_ns, unsigned* status) {
   const unsigned long long t0 = globaltimer_ns();
   for (unsigned it = 1;; ++it) {
     if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
     if ((it & 63u) == 0) {
       int given_up;
       asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(given_up) : "r"(abort_flag) : "memory");
-      const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+      const bool late = globaltimer_ns() - t0 > limit_ns;
       if (__any_sync(0xffffffffu, given_up || late)) {
         if (!given_up) set_status(status, LSA_DEV_ERR_TIMEOUT);
         asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
@@ -400,9 +404,10 @@ __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, unsigned parity, uin
     }
   }
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity, uint32_t abort_flag, unsigned* status) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity, uint32_t abort_flag, unsigned long long limit_ns,
+                                         unsigned* status) {
   if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
-  return bar_wait_slow(bar, parity, abort_flag, status);
+  return bar_wait_slow(bar, parity, abort_flag, limit_ns, status);
 }
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
   asm volatile(
@@ -736,14 +741,13 @@ constexpr int kNFull = kQEmpty + 16, kNEmpty = kNFull + 32;            // [2 pip
 constexpr int kSegFull = kNEmpty + 32, kSegDone = kSegFull + 24 * kAhead;   // [3][kAhead]
 constexpr int kDrain = kSegDone + 24 * kAhead, kMeet = kDrain + 16;            // [2], [2]: a warpgroup's warps
 constexpr int kTmemAt = kMeet + 16, kAbortAt = kTmemAt + 4, kVerdictAt = kAbortAt + 4;   // (two verdicts)
-constexpr int kGridWAt = kVerdictAt + 8;                               // CTAs of the wide list
 // The entry at the start of the wide share, or of the two narrow ones.
 struct Found {
   List s;
   int64_t r, per_head;       // the place in the entry, the entry's places per KV head
   int v;
 };
-constexpr int kFoundAt = kGridWAt + 8;
+constexpr int kFoundAt = kVerdictAt + 8;
 constexpr int kSmemBytes = kFoundAt + 2 * static_cast<int>(sizeof(Found));
 static_assert(kSmemBytes <= 232448 && sizeof(Seg) % 8 == 0 && kFoundAt % 8 == 0, "shared memory of one CTA");
 
@@ -866,7 +870,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const int me = blockIdx.x;
   // Prefix mode: sequences from `grouped` on belong to no group.
   const int grouped = plan.groups ? ld_dep(plan.cu + plan.groups) : 0;
-  if (kPrefix && me == 0 && tid == 0) *work.ok = bad ? 0 : 1;
+  if (!kFold && tid == 0) work.ok[me] = bad ? 0 : 1;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {   // the entry at the start of the wide share, or the entries of the two narrow ones
     const bool k = me < grid_w;
@@ -886,14 +890,13 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       found[x] = {s, u - at, n / kNumKVHeads, v};
     }
   }
-  if (tid == 0) *reinterpret_cast<volatile int*>(smem + kGridWAt) = grid_w;
   const bool wide = kHasWide && me < grid_w;   // what the CTA does
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = *reinterpret_cast<const volatile uint32_t*>(smem + kTmemAt);
   const Seg* const segs = reinterpret_cast<const Seg*>(smem + kSegAt);
-  auto wait = [&](int bar, unsigned parity) { return bar_wait(sm + bar, parity, abort_flag, status); };
+  auto wait = [&](int bar, unsigned parity) { return bar_wait(sm + bar, parity, abort_flag, plan.wait_ns, status); };
   // Two at once: a barrier that is ready still costs its round trip.
   auto wait2 = [&](int a, unsigned parity_a, int b, unsigned parity_b) {
     const bool ready_a = bar_try(sm + a, parity_a), ready_b = bar_try(sm + b, parity_b);
@@ -1080,7 +1083,13 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         for (unsigned i = halves > ring.mask ? halves - ring.mask - 1 : 0; i < halves; ++i)
           mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + kFull) + ring.half(i), ring.parity(i), &never);
       };
+      // A planner that withholds its share: the others wait for its segments and it
+      // for the end of their products, until the limit.
       bool ok = true;
+      if (plan.withheld == me) {
+        wait(kDrain + 8 * w, 0);
+        ok = false;
+      }
       if (wide && warp == kLoadWarp) {
         for (unsigned k = 0; ok; ++k) {
           ok = seg_get(0, k);
@@ -1098,7 +1107,7 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         begin(0, part_w, total[1], me);
         // One place stays free: in segment k the planner writes segment k + 3
         // where k - 1 was, which does not hold back the query tiles of k + 1.
-        ok = publish(0, part_w, me);
+        ok = ok && publish(0, part_w, me);
         unsigned k = 0;
         for (; ok; ++k) {
           const Seg& s = segs[k % kAhead];
@@ -1472,13 +1481,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
-  if (tid < 6 && *reinterpret_cast<const volatile int*>(smem + kAbortAt)) {
-    // A wait ran out: what the merge would read may be a former call's.
-    const int grid_wide = *reinterpret_cast<const volatile int*>(smem + kGridWAt);
-    const int me = blockIdx.x, turned = me - grid_wide + (me < grid_wide ? gridDim.x : 0);
-    if (kPrefix) *work.ok = 0;
-    else if (!kFold) work.parts[tid < 2 ? 2 * me + tid : 2 * kMaxCtas + 4 * turned + tid - 2] = make_int4(0, 0, 0, 0);
-  }
+  // A wait ran out: what the merge would read may be a former call's.
+  if (!kFold && tid == 0 && *reinterpret_cast<const volatile int*>(smem + kAbortAt)) work.ok[blockIdx.x] = 0;
   if (warp == kMmaWarp) {
     tcgen05_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1486,6 +1490,15 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // ---- the merge kernels --------------------------------------------------------
+// Whether no CTA of the call has given up: a tile's partials lie with several, and
+// one that is missing would be a former call's.  (The whole warp.)
+__device__ __forceinline__ bool call_is_whole(const Work& w, int grid, int lane) {
+  int ok = 1;
+#pragma unroll
+  for (int i = 0; i < kMaxCtas; i += 32) ok &= ld_dep(w.ok + min(i + lane, grid - 1));
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Window mode.  The queries of a split tile are shared out over the slots that
 // hold its partials.  The first kMergeY x 2 grid CTAs: kMergeY to a slot of the wide
 // shares, 2 warps (half the dims each) to a query; the others: 2 slots of the
@@ -1504,7 +1517,8 @@ window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) 
   const int wide = rest < 0;
   const int slot = wide ? blockIdx.x / kMergeY : rest * 2 + (warp >> 2);
   const uint4 a = ld_dep(reinterpret_cast<const uint4*>(work.parts + (wide ? 0 : 2 * kMaxCtas) + slot));
-  if (!a.w) return;
+  const bool whole = call_is_whole(work, grid, lane);
+  if (!a.w || !whole) return;
   const int lo = a.z & 0xffff, n = static_cast<int>(a.z >> 16) - lo + 1, cnt = static_cast<int>(a.w);
   const int half = wide ? (cnt + 1) >> 1 : cnt;   // pipeline 0's queries are in blocks 0 .., pipeline 1's in blocks 4 ..
   const int first = wide ? blockIdx.x % kMergeY * (kMergeWarps / 2) + (warp >> 1) : 0;
@@ -1526,16 +1540,16 @@ window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) 
 constexpr int kFoldParts = 4;
 template <int kBatch>
 __global__ void __launch_bounds__(32 * kFoldParts, kBatch > 8 ? 2 : 4)
-prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
+prefix_merge_kernel(const Work work, int grid, int B, __nv_bfloat16* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int pairs = B * kNumKVHeads, pair = blockIdx.x;
-  const int ok = ld_dep(work.ok);
   int ends[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) ends[i] = ld_dep(work.ends + i * static_cast<int64_t>(pairs) + pair);
-  if (!ok || ends[2] == kNone) return;   // (kNone: the output is written)
+  const bool whole = call_is_whole(work, grid, lane);
+  if (!whole || ends[2] == kNone) return;   // (kNone: the output is written)
   auto many = [&](int first, int last) {
     return first == kNone ? 0 : first & kEndWhole ? 1 : last - (first & kEndShare) + 1;
   };
@@ -1556,13 +1570,13 @@ prefix_merge_kernel(const Work work, int B, __nv_bfloat16* __restrict__ out) {
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 // The workspace's parts: counts, rows and their log-sum-exps, parts, ends, the
-// verdict.  `queries`: the most queries of an entry; `pairs`: prefix mode's.
+// verdicts.  `queries`: the most queries of an entry; `pairs`: prefix mode's.
 size_t layout(Work* w, void* at, int64_t places, int queries, int64_t pairs) {
   const int narrow = kGroup * (queries <= 4 ? queries : kNarrowQ);   // whole blocks of 4 queries, or one smaller block
   const int wide = queries <= kNarrowQ ? 0 : kGroup * kWideQ;
   const int64_t rows = places + 2ll * kMaxCtas * wide + 4ll * kMaxCtas * narrow;
   const size_t count = 2 * kMaxCtas * sizeof(int), parts = 6 * kMaxCtas * sizeof(int4);
-  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4), ends = round16(4 * pairs * 4), ok = 16;
+  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4), ends = round16(4 * pairs * 4), ok = kMaxCtas * sizeof(int);
   if (w) {
     char* p = static_cast<char*>(at);
     w->count = reinterpret_cast<int*>(p);
@@ -1587,6 +1601,9 @@ size_t prefix_layout(Work* w, void* at, int B) {
 
 std::mutex g_mu;
 bool g_attr_set[3][64] = {};
+// lsa_debug_withhold_share: the limit in microseconds and the CTA + 1 for the next
+// call, 0: none.
+std::atomic<uint64_t> g_withhold{0};
 
 int encode_pool(CUtensorMap* map, const void* base, int64_t n_slots, int rows) {
   const cuuint64_t dims[2] = {kHeadDim, static_cast<cuuint64_t>(n_slots) * kNumKVHeads * kChunkTokens};
@@ -1623,7 +1640,7 @@ int check(const void* q, const void* k_pool, const void* v_pool, int64_t n_slots
 }
 
 template <Mode kMode>
-int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool, const void* v_pool, float scale, void* out,
+int launch(Plan& plan, const Work& work, const void* q, const void* k_pool, const void* v_pool, float scale, void* out,
            int64_t most_units, void* stream) {
   const int sms = device_sm_count();
   if (sms < 2 || !tensor_map_encoder()) return LSA_ERR_NO_DEVICE;   // (wide and narrow tiles have CTAs of their own)
@@ -1657,6 +1674,9 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
   const int most = sms < kMaxCtas ? sms : kMaxCtas;
   const int64_t want = (most_units + kMinShare - 1) / kMinShare;
   const int grid = want < most ? (want < 2 ? 2 : static_cast<int>(want)) : most;
+  const uint64_t withhold = g_withhold.exchange(0);
+  plan.withheld = withhold ? static_cast<int>((withhold & 0xffffffffu) - 1) % grid : -1;
+  plan.wait_ns = withhold ? (withhold >> 32) * 1000 : kWaitLimitNs;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(out);
   launch_pdl(true, pool_attn_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, tm_k, tm_v, tm_k_part, tm_v_part,
@@ -1664,7 +1684,7 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
              scale * 1.4426950408889634f, o, lsa_device_status_ptr());
   if (kMode == kPrefixes)
     launch_pdl(true, plan.B * kNumKVHeads > 2 * sms ? prefix_merge_kernel<8> : prefix_merge_kernel<16>,
-               dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work, plan.B, o);
+               dim3(plan.B * kNumKVHeads), dim3(32 * kFoldParts), 0, s, work, grid, plan.B, o);
   else if (kMode == kWindow)
     launch_pdl(true, window_merge_kernel, dim3((2 * kMergeY + 2) * grid),
                dim3(32 * kMergeWarps), 0, s, work, grid, o);
@@ -1675,6 +1695,12 @@ int launch(const Plan& plan, const Work& work, const void* q, const void* k_pool
 }  // namespace lsa
 
 extern "C" {
+
+int lsa_debug_withhold_share(int cta, unsigned int limit_us) {
+  if (cta < -1 || limit_us == 0 || limit_us > 2000000u) return LSA_ERR_INVALID_ARG;
+  lsa::pool::g_withhold.store(cta < 0 ? 0 : static_cast<uint64_t>(limit_us) << 32 | (static_cast<unsigned>(cta) + 1u));
+  return LSA_OK;
+}
 
 size_t lsa_window_attn_workspace_size(int B, int max_q) {
   if (B <= 0 || B > LSA_MAX_BATCH || max_q <= 0) return 0;
