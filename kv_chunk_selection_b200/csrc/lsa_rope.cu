@@ -100,8 +100,11 @@ __device__ __forceinline__ int64_t pool_row(const Args& a, int64_t t, unsigned* 
 
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 5) qk_norm_rope_kernel(const Args a, unsigned* status) {
-  griddep_launch_dependents();
+  // The wait first: the next kernel may be an attention call that reads what the one
+  // before this wrote (the gather's chunks, under LSA_ATTN_KV_UNCHANGED) without a
+  // wait of its own.
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t t = blockIdx.x;
   const int hw = threadIdx.x >> 4, lane = threadIdx.x & 15;
   // This lane's two runs of 4 dims.
