@@ -1,8 +1,12 @@
-"""The pool that lsa_qk_norm_rope_pool fills, read by the chunk path."""
+"""The pool that lsa_qk_norm_rope_pool fills, read by the chunk path: scores, selection, gather and decode attention over
+the kept chunks, each checked in 64 bits."""
+import numpy as np
 import pytest
 import torch
 
 import kv_chunk_selection_b200 as lsa
+import oracle
+from lsa_testlib import assert_attention_close, assert_kept_matches, assert_scores_close, f64
 from pool_testlib import i32
 
 pytestmark = pytest.mark.gpu
@@ -52,6 +56,27 @@ class Serving:
         from kv_chunk_selection_b200.window import LayerWindow
         n = i32([-(-x // 64) for x in self.lens])
         return LayerWindow(n, self.k_per_seq, self.table, self.chunks, DEV)
+
+
+def test_the_chunk_path_over_the_filled_pool():
+    s = Serving()
+    for step in range(3):                            # a token of each sequence, then a window over what is cached
+        q = s.tokens(range(s.B), s.lens)
+        s.lens = [n + 1 for n in s.lens]
+        lw, q_idx = s.window(), bf16((s.B, 16, 128), s.g)
+        out = torch.empty((s.B, 64, 128), device=DEV)
+        lw.select(q_idx, s.w, s.keys)
+        lw.gather(s.kp, s.vp)
+        lw.attend(q, out)
+        torch.cuda.synchronize()
+        assert lsa.read_device_status() == 0
+        n = [-(-x // 64) for x in s.lens]
+        scores = oracle.index_scores(f64(q_idx), f64(s.w), f64(s.keys), s.table.cpu().numpy(), np.array(n), s.chunks)
+        assert_scores_close(lw.scores, scores, n)
+        kept = lw.kept_lists()
+        assert_kept_matches(kept, scores, n, s.k_per_seq.tolist())
+        k, v, cu = oracle.gather_chunks(f64(s.kp), f64(s.vp), s.table.cpu().numpy(), kept, s.chunks)
+        assert_attention_close(out, oracle.sparse_decode_attn(f64(q), k, v, cu))
 
 
 def test_the_norms_between_a_gather_and_an_attention_that_reads_ahead():
