@@ -765,8 +765,9 @@ def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, m
     """out[t] = attention of query row t over the last ``window`` tokens up to its own and the first ``n_sink``.
 
     Sequence b's queries are rows cu_q[b] .. cu_q[b+1]-1 of q [T, 64, 128] and the last of its seq_len[b] cached
-    tokens, which the pools [slots, 8, 64, 128] hold by chunk_table [B, max_chunks] (None: identity layout); at
-    most ``max_q`` per sequence.  out is bf16 like q; workspace from new_window_attn_workspace(B, max_q)."""
+    tokens, which the pools [slots, 8, 64, 128] hold by chunk_table [B, max_chunks] (None: identity layout, where
+    ``max_chunks`` has to be given; with a table it may be None); at most ``max_q`` per sequence.  out
+    is bf16 like q; workspace from new_window_attn_workspace(B, max_q)."""
     dev = _current_device()
     if not _is(_pool_attn_fits, q, k_pool, v_pool, chunk_table, seq_len, max_chunks, out, workspace, dev):
         _pool_attn_explain(q, k_pool, v_pool, chunk_table, seq_len, max_chunks, out, workspace, "seq_len")
@@ -777,7 +778,8 @@ def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, m
         raise ValueError("cu_q must be [B + 1]")
     st = (_lib or _load()).lsa_window_attn(
         q.data_ptr(), q.shape[0], k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], _at(chunk_table),
-        cu_q.data_ptr(), seq_len.data_ptr(), B, max_chunks, max_q, window, n_sink,
+        cu_q.data_ptr(), seq_len.data_ptr(), B, max_chunks if chunk_table is None else chunk_table.shape[1], max_q, window,
+        n_sink,
         _ATTN_SCALE if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
         workspace.numel(), _stream_of(stream, dev))
     if st:
