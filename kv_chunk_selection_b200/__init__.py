@@ -641,6 +641,11 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _int32(x):
+    """The nearest number that a C int holds: ctypes would take the low 32 bits."""
+    return x if -0x80000000 <= x <= 0x7fffffff else 0x7fffffff if x > 0 else -0x80000000
+
+
 def lsa_qk_norm_rope(qkv, positions, inv_freq, q_out, k_out, v_out=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, rope_scale=1.0, stream=None):
     """Head norms and rotary positions of a fused projection's rows qkv [T, 80 * 128] (rows may lie further
@@ -711,7 +716,7 @@ def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk
         qkv.data_ptr(), _row_stride(qkv), T, _at(q_weight), _at(k_weight), eps, _at(positions), _at(inv_freq),
         0 if inv_freq is None else 2 * inv_freq.numel(), rope_scale, ROPE_INTERLEAVED if interleaved else 0,
         q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), n_slots, _at(chunk_table), seq_ids.data_ptr(),
-        cache_pos.data_ptr(), B, max_chunks, _stream_of(stream, dev))
+        cache_pos.data_ptr(), B, _int32(max_chunks), _stream_of(stream, dev))
     if st:
         raise LsaError("lsa_qk_norm_rope_pool", st)
 
@@ -719,7 +724,7 @@ def lsa_qk_norm_rope_pool(qkv, positions, inv_freq, q_out, k_pool, v_pool, chunk
 def new_window_attn_workspace(B: int, max_q: int, device=None) -> torch.Tensor:
     """A workspace for lsa_window_attn with up to ``max_q`` queries per sequence, zeroed (every call leaves its
     counts zero)."""
-    n = int(_load().lsa_window_attn_workspace_size(int(B), int(max_q)))
+    n = int(_load().lsa_window_attn_workspace_size(_int32(int(B)), _int32(int(max_q))))
     if n == 0:
         raise ValueError("unsupported batch")
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
@@ -778,8 +783,8 @@ def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, m
         raise ValueError("cu_q must be [B + 1]")
     st = (_lib or _load()).lsa_window_attn(
         q.data_ptr(), q.shape[0], k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], _at(chunk_table),
-        cu_q.data_ptr(), seq_len.data_ptr(), B, max_chunks if chunk_table is None else chunk_table.shape[1], max_q, window,
-        n_sink,
+        cu_q.data_ptr(), seq_len.data_ptr(), B, _int32(max_chunks) if chunk_table is None else chunk_table.shape[1],
+        _int32(max_q), _int32(window), _int32(n_sink),
         _ATTN_SCALE if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
         workspace.numel(), _stream_of(stream, dev))
     if st:
@@ -788,7 +793,7 @@ def lsa_window_attn(q, k_pool, v_pool, chunk_table, cu_q, seq_len, max_chunks, m
 
 def new_prefix_attn_workspace(B: int, n_groups: int, device=None) -> torch.Tensor:
     """A workspace for lsa_prefix_decode_attn (it needs no initialisation)."""
-    n = int(_load().lsa_prefix_attn_workspace_size(int(B), int(n_groups)))
+    n = int(_load().lsa_prefix_attn_workspace_size(_int32(int(B)), _int32(int(n_groups))))
     if n == 0:
         raise ValueError("unsupported batch")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -828,7 +833,7 @@ def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len
     st = (_lib or _load()).lsa_prefix_decode_attn(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], _at(prefix_table), _at(cu_group),
         _at(prefix_len), groups, chunks, _at(chunk_table), suffix_len.data_ptr(), B,
-        max_chunks if chunk_table is None else chunk_table.shape[1],
+        _int32(max_chunks) if chunk_table is None else chunk_table.shape[1],
         _ATTN_SCALE if softmax_scale is None else softmax_scale, out.data_ptr(), workspace.data_ptr(),
         workspace.numel(), _stream_of(stream, dev))
     if st:

@@ -63,3 +63,31 @@ def test_window_takes_its_chunks_from_the_table(rec):
         window(rec, None, table=False)
     with pytest.raises(ValueError, match="chunk_table"):
         window(rec, 4)
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 70])
+def test_numbers_past_32_bits_are_the_largest_number(rec, big):
+    """Not what their low 32 bits say: a window, a count of sinks and a bound of queries that are larger than any
+    sequence mean all of it; a table's width is refused by the library."""
+    args = window(rec, big, window=big, sinks=big, max_q=big, table=False)
+    assert args == dict(B=2, max_chunks=2 ** 31 - 1, max_q=2 ** 31 - 1, window=2 ** 31 - 1, n_sink=2 ** 31 - 1)
+    args = window(rec, 5, window=-big, sinks=-big, max_q=-big)
+    assert args["window"] < 0 and args["n_sink"] < 0 and args["max_q"] < 0
+
+
+@pytest.mark.parametrize("big", [2 ** 32 + 5, 2 ** 70])
+def test_widths_past_32_bits_in_the_other_calls(rec, big):
+    q, pool, qkv = bf16(2, 64, 128), bf16(2, 8, 64, 128), bf16(2, 80 * 128)
+    lsa.lsa_prefix_decode_attn(q, pool, pool, None, None, None, None, i32(2), torch.empty_like(q),
+                               torch.zeros(16, dtype=torch.uint8), max_chunks=big)
+    assert rec.calls[-1][1][11:13] == [2, 2 ** 31 - 1]
+    lsa.lsa_qk_norm_rope_pool(qkv, None, None, q, pool, pool.clone(), None, i32(2), i32(2), big)
+    assert rec.calls[-1][1][18:20] == [1, 2 ** 31 - 1]
+
+
+def test_a_workspace_for_any_bound_of_queries(monkeypatch):
+    sizes = []
+    monkeypatch.setattr(torch, "zeros", lambda n, **kw: sizes.append(n))
+    lsa.new_window_attn_workspace(2, 1 << 20)
+    lsa.new_window_attn_workspace(2, 2 ** 32 + 1)
+    assert sizes[0] == sizes[1]
