@@ -592,11 +592,11 @@ _POOL_ROWS = (NUM_KV_HEADS, CHUNK_TOKENS, HEAD_DIM)
 
 
 def _rope_fits(qkv, positions, inv_freq, q_out, q_weight, k_weight, dev: int) -> bool:
-    T = qkv.shape[0]
     return (qkv.dtype is torch.bfloat16 and qkv.get_device() == dev and qkv.dim() == 2 and qkv.shape[1] == _QKV_WIDTH
-            and qkv.stride(1) == 1 and _fits(q_out, torch.bfloat16, dev) and q_out.shape == (T, NUM_Q_HEADS, HEAD_DIM)
+            and qkv.stride(1) == 1 and _fits(q_out, torch.bfloat16, dev)
+            and q_out.shape == (qkv.shape[0], NUM_Q_HEADS, HEAD_DIM)
             and (inv_freq is None or (_fits(inv_freq, torch.float32, dev) and inv_freq.dim() == 1
-                                      and _fits(positions, torch.int32, dev) and positions.numel() == T))
+                                      and _fits(positions, torch.int32, dev) and positions.numel() == qkv.shape[0]))
             and (q_weight is None or (_fits(q_weight, torch.float32, dev) and q_weight.numel() == HEAD_DIM))
             and (k_weight is None or (_fits(k_weight, torch.float32, dev) and k_weight.numel() == HEAD_DIM)))
 

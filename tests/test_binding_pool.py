@@ -91,3 +91,10 @@ def test_a_workspace_for_any_bound_of_queries(monkeypatch):
     lsa.new_window_attn_workspace(2, 1 << 20)
     lsa.new_window_attn_workspace(2, 2 ** 32 + 1)
     assert sizes[0] == sizes[1]
+
+
+def test_rows_of_any_other_rank_are_refused_by_name(rec, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    for shape in ((), (80 * 128,), (1, 1, 80 * 128)):
+        with pytest.raises(ValueError, match="qkv"):
+            lsa.lsa_qk_norm_rope(bf16(*shape), None, None, bf16(1, 64, 128), bf16(1, 8, 128))
