@@ -702,7 +702,8 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
  *                prefix_len device int32 [n_groups].  n_groups 0: all may be NULL
  *   chunk_table  device int32 [B][max_chunks] or NULL (identity layout), slots
  *                of the sequence's own chunks (its own token 0 is token 0 of
- *                chunk 0, whatever the prefix's length); suffix_len device
+ *                chunk 0, whatever the prefix's length); NULL with max_chunks 0:
+ *                no sequence has a chunk of its own yet.  suffix_len device
  *                int32 [B]
  *   workspace    device, >= lsa_prefix_attn_workspace_size(B, n_groups) bytes,
  *                16-byte aligned, no initialisation; calls that may overlap on

@@ -812,7 +812,8 @@ def lsa_prefix_decode_attn(q, k_pool, v_pool, prefix_table, cu_group, prefix_len
     of its own chunks chunk_table[b], all in the pools [slots, 8, 64, 128].
 
     q and out [B, 64, 128] bf16; prefix_table, cu_group and prefix_len None: no sequence has a prefix; chunk_table
-    None: the identity layout with ``max_chunks`` chunks per sequence.  Workspace from new_prefix_attn_workspace."""
+    None: the identity layout with ``max_chunks`` chunks per sequence; before the first own token the table may be
+    [B, 0].  Workspace from new_prefix_attn_workspace."""
     dev = _current_device()
     if not _is(_pool_attn_fits, q, k_pool, v_pool, chunk_table, suffix_len, max_chunks, out, workspace, dev):
         _pool_attn_explain(q, k_pool, v_pool, chunk_table, suffix_len, max_chunks, out, workspace, "suffix_len")

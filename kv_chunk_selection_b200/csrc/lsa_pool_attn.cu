@@ -1629,8 +1629,9 @@ int encode_q(CUtensorMap* map, const void* base, int64_t rows, int queries) {
 
 // Checks of the arguments that both calls share.
 int check(const void* q, const void* k_pool, const void* v_pool, int64_t n_slots, const int32_t* len, int B, int max_chunks,
-          float scale, const void* out) {
-  if (!q || !k_pool || !v_pool || !len || !out || n_slots <= 0 || B <= 0 || max_chunks <= 0) return LSA_ERR_INVALID_ARG;
+          int least_chunks, float scale, const void* out) {
+  if (!q || !k_pool || !v_pool || !len || !out || n_slots <= 0 || B <= 0 || max_chunks < least_chunks)
+    return LSA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !isfinite(scale)) return LSA_ERR_INVALID_ARG;
   if (B > LSA_MAX_BATCH) return LSA_ERR_UNSUPPORTED_SHAPE;
   // Positions and TMA rows (n_slots * 512) are 32-bit.
@@ -1713,7 +1714,7 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
                     void* stream) {
   using namespace lsa;
   if (!cu_q || T <= 0 || max_q <= 0 || window <= 0 || n_sink < 0) return LSA_ERR_INVALID_ARG;
-  const int st = pool::check(q, k_pool, v_pool, n_slots, seq_len, B, max_chunks, softmax_scale, out);
+  const int st = pool::check(q, k_pool, v_pool, n_slots, seq_len, B, max_chunks, 1, softmax_scale, out);
   if (st != LSA_OK) return st;
   if (T > (int64_t{1} << 30)) return LSA_ERR_UNSUPPORTED_SHAPE;
   if (!workspace || workspace_bytes < pool::window_layout(nullptr, nullptr, max_q)) return LSA_ERR_WORKSPACE;
@@ -1757,7 +1758,8 @@ int lsa_prefix_decode_attn(const void* q, const void* k_pool, const void* v_pool
   using namespace lsa;
   if (n_groups < 0 || n_groups > B || (n_groups > 0 && (!prefix_table || !cu_group || !prefix_len || max_prefix_chunks <= 0)))
     return LSA_ERR_INVALID_ARG;
-  const int st = pool::check(q, k_pool, v_pool, n_slots, suffix_len, B, max_chunks, softmax_scale, out);
+  // (Without a table there may be no own chunks at all: before the first own token.)
+  const int st = pool::check(q, k_pool, v_pool, n_slots, suffix_len, B, max_chunks, chunk_table ? 1 : 0, softmax_scale, out);
   if (st != LSA_OK) return st;
   if (max_prefix_chunks > (1 << 23)) return LSA_ERR_UNSUPPORTED_SHAPE;
   if (!workspace || workspace_bytes < pool::prefix_layout(nullptr, nullptr, B)) return LSA_ERR_WORKSPACE;
