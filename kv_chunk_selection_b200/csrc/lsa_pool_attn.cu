@@ -549,8 +549,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 // 2^x of two values at most kRaise, by the FMA pipe: floor by an addition that
 // rounds down, a polynomial of degree 4 for 2^f on [0, 1) with value 1 at 0
-// (minimax for the relative error: 2.9e-6, against 2^-9 of the rounding to bf16
-// that follows), and the integer part added to the exponent.  From -127 down
+// (minimax for the relative error: 2.9e-6, against up to 2^-8 of the rounding to
+// bf16 that follows), and the integer part added to the exponent.  From -127 down
 // (masked scores among them) exactly 0.
 __device__ __forceinline__ void exp2_fma(uint64_t x, float& a, float& b) {
   float lo, hi;
@@ -1365,8 +1365,8 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               b = fast_exp2(b);
             }
             sum[c & 3] = add2(sum[c & 3], pack2(a, b));
-            // One rounding of the probabilities to bf16, half a step (2^-9) at
-            // most: the output is rounded to the same type.
+            // One rounding of the probabilities to bf16, half a step (2^-8 of the
+            // value) at most: the output is rounded to the same type.
             pk[c] = __uint_as_float(pack_bf16(a, b));
           }
           tmem_st32(sp, pk);

@@ -25,8 +25,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     * ``"base"``: the base multiplied by factor^(rot_dim / (rot_dim - 2)), which leaves the fastest pair alone and
       divides the slowest one by ``factor``;
     * ``"parts"``: by the turns r that a pair makes in ``original_context`` tokens: r > ``fast`` stays, r < ``slow``
-      is divided by ``factor``, a linear ramp between them; ``rope_scale`` = 0.1 ln(factor) + 1 (interpolation by
-      parts, Peng et al. 2023, "YaRN", section 3).
+      is divided by ``factor``, a linear ramp in r between them; ``rope_scale`` = 0.1 ln(factor) + 1 (interpolation by
+      parts, Peng et al. 2023, "YaRN", section 3).  Tables that ramp linearly in the pair's index i instead, between
+      the two bounds' indexes, differ from these inside the ramp: a model trained with such a table needs its own.
 
     Computed in fp64 and rounded once to fp32.
     """
