@@ -593,8 +593,9 @@ int lsa_gather_tokens(const void* k_buf, const void* v_buf, int64_t buf_chunks, 
  *
  * where (a, b) are dims (i, i + rot_dim / 2) of y, or dims (2i, 2i + 1) with
  * LSA_ROPE_INTERLEAVED; dims rot_dim .. 127 keep y.  The value heads are
- * copied.  fp32, rounded once to bf16; the angle is formed in fp64, so far
- * positions keep their phase.  Scaled rotations for long contexts are a matter
+ * copied.  fp32, rounded once to bf16 (a head whose squares overflow fp32,
+ * values past about 1e18, comes out as zeros); the angle is formed in fp64, so
+ * far positions keep their phase.  Scaled rotations for long contexts are a matter
  * of inv_freq and rope_scale (the Python binding's rope_frequencies).
  *   qkv        device bf16 [T] rows of 80 * 128 values, row_stride (>= 10240, a
  *              multiple of 8) values apart
@@ -651,7 +652,8 @@ int lsa_qk_norm_rope_pool(const void* qkv, int64_t row_stride, int64_t T, const 
  *   q           device bf16 [T][64][128]; out device bf16 [T][64][128] (fp32
  *               sums and softmax; the probabilities are rounded once to bf16
  *               for the tensor cores, the output once).  Rows at or past
- *               cu_q[B] are left as they were.
+ *               cu_q[B] are left as they were.  out must not overlap q or the
+ *               pools
  *   k_pool, v_pool  device bf16 [n_slots][8][64][128], n_slots < 2^22
  *   chunk_table device int32 [B][max_chunks] or NULL (identity layout); chunks
  *               that no query sees are not looked up: a table may hold -1 where
@@ -696,7 +698,7 @@ int lsa_window_attn(const void* q, int64_t T, const void* k_pool, const void* v_
  * cu_group[n_groups] on belong to no group: they attend their own tokens only.
  * A sequence with no token at all gets zeros (infinite scores as above).
  *   q            device bf16 [B][64][128]; out device bf16 [B][64][128]
- *                (rounded as by lsa_window_attn)
+ *                (rounded as by lsa_window_attn; must not overlap q or the pools)
  *   prefix_table device int32 [n_groups][max_prefix_chunks], slots of the
  *                prefix's chunks; cu_group device int32 [n_groups+1];
  *                prefix_len device int32 [n_groups].  n_groups 0: all may be NULL

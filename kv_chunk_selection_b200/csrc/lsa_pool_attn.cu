@@ -19,20 +19,20 @@
 // CTA for the wide list, two per CTA for the narrow one.  So one token over a long
 // window, a ragged batch and a long prompt all fill the chip evenly.  A call with
 // both gives each list its own CTAs, as many as its units cost (every CTA with a
-// share of both, one after the other: 32 sequences over a prefix of 32768 tokens
-// and up to 1024 of their own took 67 us, now 60; 33 queries over 512 tokens 22.7,
-// now 18.1).  A tile that a cut splits leaves partials (normalised rows and their
-// log-sum-exps), which are folded in the order of the shares, so that the result
-// does not depend on timing: by the share that adds a tile's last one where that
-// is little for one SM (single tokens: no second launch), else by a second kernel
-// (32 sequences over a prefix of 32768 tokens leave 19 MB).
+// share of both, one after the other, takes 12% longer for 32 sequences over a prefix
+// of 32768 tokens and up to 1024 of their own, 25% for 33 queries over 512 tokens).
+// A tile that a cut splits leaves partials (normalised rows and their log-sum-exps),
+// which are folded in the order of the shares, so that the result does not depend on
+// timing: by the share that adds a tile's last one where that is little for one SM
+// (single tokens: no second launch), else by a second kernel (32 sequences over a
+// prefix of 32768 tokens leave 19 MB).
 //
 // A CTA (one per SM, 12 warps) has two pipelines w = 0, 1 of
 //   warps 4w..4w+3  a softmax warpgroup, a thread per row: the scores of a unit
 //                   come from TMEM, the probabilities go back in their place as
 //                   bf16.  The running maximum is only raised when it grows by
-//                   more than 2^8 (the sums stay exact, the accumulator is
-//                   rescaled rarely);
+//                   2^8 or more (the sums stay exact, the accumulator is rescaled
+//                   rarely);
 //   warp 8 + w      issues the tcgen05.mma: S = Q K^T (128 x 64 x 128) into one
 //                   of two score buffers, O += P V (128 x 128 x 64) with P from
 //                   TMEM;
@@ -46,13 +46,16 @@
 // product are theirs.
 //
 // What bounds it.  Narrow shares: memory (one token over 100000: 70.6 us, 5.8 TB/s,
-// 89% of the copy rate; 64 tokens over windows of 1024: 54.5 us, 4.9 TB/s, the rest is
+// 89% of the copy rate; 64 tokens over windows of 1024: 55.0 us, 4.9 TB/s, the rest is
 // the start, 5 us, and the spread of the CTAs' ends).  Wide shares: the chain of a
 // unit, 1450 cycles for 128 x 2 rows, of which the tensor core is busy 1350 (with
-// 64 keys a product of scores is fed by shared memory); without the softmax's
-// arithmetic a prompt of 4096 queries over a window of 1024 would take 92% of its
-// 137 us (0.88 PFLOP/s).  Single tokens over short contexts: latency, about 5 us until
-// the first scores, 1.5 us a unit, 2 us for the fold.
+// 64 keys a product of scores is fed by shared memory: 48 KiB in 384 cycles for 256 of
+// products); and what is no unit: of the 139.6 us of a prompt of 4096 queries over a
+// window of 1024 (0.86 PFLOP/s) its 108 units a CTA are about 82, the ends of 7 tiles
+// some 25, the merge 11, the start 5 to 7.  Without the softmax's arithmetic it would
+// take 92%.  Single tokens over short contexts: latency, about 5 us until the first
+// scores, 1.5 us a unit, 2 us for the fold.  (Times are of calls in a row; a single one
+// after a flush of the L2 cache takes 5 to 25 us longer.)
 //
 // TMEM (512 columns): scores 2 pipelines x 2 buffers x 64, accumulators 2 x 128.
 // Rows that no query of a tile sees are zeroed in V's stage before the product,
@@ -1018,9 +1021,9 @@ pool_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       // K and V of a segment's units, the next ones of the share.  In window mode only
       // the parts (16 tokens) of a chunk with a token in sight are loaded; what the
       // other rows hold is masked (K) and zeroed (V).  64 single tokens over windows of
-      // 1024 take 54.4 us so, 56.5 with whole chunks (300 MB for 269), a prompt of 4096
-      // 139.7 and 142.9.  A prefix call has only ends of sequences to save on, and
-      // takes longer by more but smaller loads (128 sequences, 5 groups: 80.1, 77.5).
+      // 1024 take 4% less time so than with whole chunks (275 MB read, 300), a prompt of
+      // 4096 2%.  A prefix call has only ends of sequences to save on, and takes longer by
+      // more but smaller loads (128 sequences, 5 groups: 3%).
       auto load_units = [&](int units, int flags, int j0, int first, int low, int g, const int32_t* table, int64_t ident,
                             int p0, int cnt) {
         // Another tile of the entry reads the same chunks: they stay in L2.
@@ -1535,8 +1538,8 @@ window_merge_kernel(const Work work, int grid, __nv_bfloat16* __restrict__ out) 
 // Prefix mode: a CTA of 4 warps per (sequence, KV head), a quarter of the dims
 // each: the partials of its group's tile, then those of its own tokens.
 // kBatch partials at a time: 16 while the CTAs of 2 an SM are all that there are,
-// 8 beyond.  16 (8): 9 sequences 19.6 (21.8) us, 32 over a prefix of 32768 tokens 54
-// (55), 128 under 16 prefixes of up to 1000 45.8 (42.7).
+// 8 beyond.  16 (8): 9 sequences 19.6 (21.8) us, 128 under 16 prefixes of up to 1000
+// 45.8 (42.7); 32 over a prefix of 32768 tokens 2% less than with 8.
 constexpr int kFoldParts = 4;
 template <int kBatch>
 __global__ void __launch_bounds__(32 * kFoldParts, kBatch > 8 ? 2 : 4)

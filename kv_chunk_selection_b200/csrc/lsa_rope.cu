@@ -21,12 +21,12 @@
 // the half layout, 8l .. 8l+7 in the interleaved one.  The lane's 4 (cos, sin)
 // are then the same for all of its heads.  The block computes each of the token's
 // once, while the loads of the heads are in flight, and passes them on in shared
-// memory (every half-warp its own: 68% of the issue slots, 59.2 us for 8191 tokens).
+// memory (58% of the issue slots; every half-warp its own: 68%, and 2% slower).
 //
 // The bytes bound it: 20 KiB read and 20 KiB written per token.  8191 tokens into
-// the pool take 57.8 us, 5.8 TB/s, 89% of the copy rate; one token takes 2.9 us,
-// a launch and two rounds to memory.  5 blocks an SM (48 registers): with 4 (60)
-// 61.9 us, with 6 (40, spilled) 69.
+// the pool take 58.4 us in a row, 5.7 TB/s, 88% of the copy rate; one token 2.9 us,
+// a launch and two rounds to memory.  5 blocks an SM (48 registers, 24 bytes of
+// them spilled in the half layout): with 4 (60) 7% slower, with 6 (40) 19%.
 #include <math.h>
 
 #include "lsa_common.cuh"
