@@ -45,8 +45,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     if scaling == "linear":
         freq = freq / factor
     elif scaling == "parts":
-        if not original_context or not 0 < original_context < math.inf or not 0 <= slow < fast < math.inf:
-            raise ValueError("scaling by parts needs a finite original_context > 0 and finite 0 <= slow < fast")
+        if not original_context or not original_context > 0 or not 0 <= slow < fast:   # (NaN too)
+            raise ValueError("scaling by parts needs original_context > 0 and 0 <= slow < fast")
         turns = original_context * freq / (2 * math.pi)
         keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
         freq = freq * keep + freq / factor * (1 - keep)
