@@ -1579,7 +1579,8 @@ size_t layout(Work* w, void* at, int64_t places, int queries, int64_t pairs) {
   const int wide = queries <= kNarrowQ ? 0 : kGroup * kWideQ;
   const int64_t rows = places + 2ll * kMaxCtas * wide + 4ll * kMaxCtas * narrow;
   const size_t count = 2 * kMaxCtas * sizeof(int), parts = 6 * kMaxCtas * sizeof(int4);
-  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4), ends = round16(4 * pairs * 4), ok = kMaxCtas * sizeof(int);
+  const size_t o = static_cast<size_t>(rows) * kHeadDim * 4, lse = round16(rows * 4);
+  const size_t ends = round16(4 * pairs * 4), ok = kMaxCtas * sizeof(int);
   if (w) {
     char* p = static_cast<char*>(at);
     w->count = reinterpret_cast<int*>(p);
